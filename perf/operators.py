@@ -1,0 +1,385 @@
+"""The 8-bit KV cache's operators as they are measured: writing it, reading it back, and attention over it.
+
+Cache (as in include/attn_b200.h): codes [pages][page][Hkv][D], uint8 holding E4M3 codes or int8, and one fp32 scale
+per (page, block of tokens, KV head); a stored value is scale * code. ``own`` picks between the plain forms below and
+the library's kernels.
+"""
+
+import math
+import random
+
+import torch
+
+own = False
+
+#: largest code value of each format
+QMAX = {"e4m3": 448.0, "int8": 127.0}
+#: scales are at least 2 ** SCALE_MIN
+SCALE_MIN = -100
+
+
+# ------------------------------------------------------------------ cases
+
+def listed():
+    return [
+        # a chat's first tokens: one sequence, one short split; the latency of a decode step
+        dict(name="decode_one_short", op="decode", fmt="e4m3", N=1, Hq=32, Hkv=8, D=128, page=16, block=16,
+             lo=100, hi=300, lens=1),
+        # a serving batch in the middle of its answers (the library's paged GQA decode batch, at 8 bits)
+        dict(name="decode_batch_e4m3", op="decode", fmt="e4m3", N=64, Hq=32, Hkv=8, D=128, page=16, block=16,
+             lo=512, hi=8192, lens=2),
+        # the same batch with integer codes, larger pages and one scale per page
+        dict(name="decode_batch_int8", op="decode", fmt="int8", N=64, Hq=32, Hkv=8, D=128, page=64, block=64,
+             lo=512, hi=8192, lens=3),
+        # one user with a long document: few rows, a long axis
+        dict(name="decode_long_int8", op="decode", fmt="int8", N=1, Hq=32, Hkv=8, D=128, page=16, block=16,
+             lo=32768, hi=32771, lens=4),
+        # a model without shared heads and with small ones, ragged and odd lengths
+        dict(name="decode_mha_d64", op="decode", fmt="e4m3", N=27, Hq=12, Hkv=12, D=64, page=32, block=16,
+             lo=0, hi=2999, lens=5),
+        # a decode step writes one token for each sequence of a batch
+        dict(name="append_step", op="append", fmt="e4m3", N=64, T=1, Hkv=8, D=128, page=16, block=16,
+             lo=512, hi=2048, lens=6),
+        # prompts being written, behind prefixes of odd lengths
+        dict(name="append_prompts", op="append", fmt="int8", N=8, T=4096, Hkv=8, D=128, page=64, block=16,
+             lo=1, hi=1000, lens=7),
+        # short odd chunks with small heads and large blocks
+        dict(name="append_odd_d64", op="append", fmt="e4m3", N=5, T=333, Hkv=3, D=64, page=128, block=128,
+             lo=0, hi=700, lens=8),
+        # a batch's whole cache read back
+        dict(name="read_batch", op="read", fmt="e4m3", N=16, Hkv=8, D=128, page=16, block=16,
+             lo=512, hi=8192, lens=9),
+        # a short prefix read back
+        dict(name="read_short_int8", op="read", fmt="int8", N=3, Hkv=5, D=64, page=32, block=32,
+             lo=1, hi=500, lens=10),
+        # chunked prefill: 2048 new tokens behind cached prefixes
+        dict(name="prefill_chunk", op="prefill", fmt="e4m3", N=4, Sq=2048, Hq=32, Hkv=8, D=128, page=16, block=16,
+             lo=2048, hi=8192, lens=11),
+        # the odd tail of a prompt, small heads
+        dict(name="prefill_tail_int8", op="prefill", fmt="int8", N=3, Sq=117, Hq=16, Hkv=4, D=64, page=32, block=32,
+             lo=117, hi=2500, lens=12),
+    ]
+
+
+def _log(rng, lo, hi):
+    return int(round(math.exp(rng.uniform(math.log(lo), math.log(hi)))))
+
+
+def draw(rng):
+    op = rng.choice(["decode", "decode", "append", "read", "prefill"])
+    page = rng.choice([16, 32, 64, 128, 256])
+    block = rng.choice([b for b in (16, 32, 64, 128, 256) if b <= page])
+    D = rng.choice([64, 128])
+    Hkv = rng.choice([1, 2, 3, 4, 5, 8, 8, 16])
+    c = dict(op=op, fmt=rng.choice(["e4m3", "int8"]), Hkv=Hkv, D=D, page=page, block=block,
+             lens=rng.randrange(1 << 30))
+    most = 64 * 4352 * 8 * 128          # values of K in the largest decode batch, on average
+    N = _log(rng, 1, 96)
+    if op in ("decode", "prefill"):
+        c["Hq"] = Hkv * rng.choice([1, 2, 4, 8, 16] if Hkv <= 8 else [1, 2, 4])
+    if op == "decode":
+        top = max(1, min(40000, most // (N * Hkv * D)))
+        hi = _log(rng, 1, top)
+        c.update(N=N, lo=rng.choice([0, hi // 16, hi // 2]), hi=hi)
+    elif op == "read":
+        N = min(N, 32)
+        hi = _log(rng, 1, max(1, min(8192, most // (8 * N * Hkv * D))))
+        c.update(N=N, lo=hi // 8, hi=hi)
+    elif op == "append":
+        T = _log(rng, 1, max(1, min(4096, most // (10 * N * Hkv * D))))
+        c.update(N=N, T=T, lo=0, hi=_log(rng, 1, 1000))
+    else:
+        N = min(N, 8)
+        room = 4 * 2048 * 5000 * 32 * 128 // (N * c["Hq"] * D)      # query-key pairs of the largest chunk
+        Sq = _log(rng, 1, min(2048, math.isqrt(room)))
+        hi = min(8192, room // Sq, Sq + _log(rng, 1, 6000))
+        c.update(N=N, Sq=Sq, lo=Sq, hi=hi)
+    return c
+
+
+def _lens(c):
+    """The batch's token counts: part of the case, so that work() knows them."""
+    r = random.Random(c["lens"])
+    return [r.randint(c["lo"], c["hi"]) for _ in range(c["N"])]
+
+
+# ------------------------------------------------------------------ inputs
+
+def _codes_of(x, scale, fmt):
+    """Codes of x at a power-of-two scale (the division is exact), rounded to nearest, ties to even."""
+    y = x / scale
+    if fmt == "e4m3":
+        return y.clamp(-448.0, 448.0).to(torch.float8_e4m3fn).view(torch.uint8)
+    return torch.round(y).clamp(-127.0, 127.0).to(torch.int8)
+
+
+def _values_of(codes, fmt):
+    return codes.view(torch.float8_e4m3fn).float() if fmt == "e4m3" else codes.float()
+
+
+def _scale_of(amax, fmt):
+    """The smallest power of two s with amax <= QMAX * s, at least 2 ** SCALE_MIN."""
+    m, e = torch.frexp(amax)
+    top, te = math.frexp(QMAX[fmt])
+    e = torch.where(amax > 0, e - te + (m > top).to(e.dtype), SCALE_MIN).clamp_min(SCALE_MIN)
+    return ((e + 127) << 23).view(torch.float32)                                # 2 ** e, exactly
+
+
+def _pool(g, pages, c, dev):
+    """One quantised pool: values whose size differs by head and by block, as a layer's keys and values do."""
+    page, block, Hkv, D = c["page"], c["block"], c["Hkv"], c["D"]
+    x = torch.randn(pages, page // block, block, Hkv, D, generator=g, device=dev)
+    x *= torch.exp(0.3 * torch.randn(1, 1, 1, Hkv, 1, generator=g, device=dev))
+    x *= torch.exp(0.2 * torch.randn(pages, page // block, 1, Hkv, 1, generator=g, device=dev))
+    scale = _scale_of(x.abs().amax(dim=(2, 4), keepdim=True), c["fmt"])
+    codes = _codes_of(x, scale, c["fmt"]).reshape(pages, page, Hkv, D)
+    return codes, scale.reshape(pages, page // block, Hkv).contiguous()
+
+
+def prepare(case, seed):
+    c, dev = case, torch.device("cuda", torch.cuda.current_device())
+    g = torch.Generator(device=dev).manual_seed(seed)
+    lens = _lens(c)
+    need = [-(-(L + c.get("T", 0)) // c["page"]) for L in lens]      # append writes behind the cached tokens
+    used, most = sum(need), max(1, max(need))
+    pages = used + max(1, used // 16)
+    perm = torch.randperm(pages, generator=g, device=dev).to(torch.int32)
+    # each sequence's pages in the order in which the pool gave them out, -1 behind them
+    n = torch.tensor(need, device=dev)
+    at = torch.arange(most, device=dev)[None, :] + (torch.cumsum(n, 0) - n)[:, None]
+    table = torch.where(torch.arange(most, device=dev)[None, :] < n[:, None], perm[at.clamp_max(pages - 1)], -1)
+    s = dict(case=c, table=table.to(torch.int32).contiguous(),
+             lens=torch.tensor(lens, dtype=torch.int32, device=dev))
+    s["kc"], s["ks"] = _pool(g, pages, c, dev)
+    s["vc"], s["vs"] = _pool(g, pages, c, dev)
+    N, Hkv, D = c["N"], c["Hkv"], c["D"]
+    if c["op"] == "append":
+        s["k_new"] = (1.5 * torch.randn(N, c["T"], Hkv, D, generator=g, device=dev)).to(torch.bfloat16)
+        s["v_new"] = (1.5 * torch.randn(N, c["T"], Hkv, D, generator=g, device=dev)).to(torch.bfloat16)
+    elif c["op"] == "read":
+        s["k_out"] = torch.zeros(N, max(1, max(lens)), Hkv, D, dtype=torch.bfloat16, device=dev)
+        s["v_out"] = torch.zeros_like(s["k_out"])
+    else:
+        rows = (N, c["Hq"], D) if c["op"] == "decode" else (N, c["Sq"], c["Hq"], D)
+        s["q"] = torch.randn(rows, generator=g, device=dev).to(torch.bfloat16)
+    return s
+
+
+# ------------------------------------------------------------------ one pass
+
+def run(state):
+    return {"decode": _decode, "append": _append, "read": _read, "prefill": _prefill}[state["case"]["op"]](state)
+
+
+def _gather(s, codes, scales):
+    """The sequences' cached values, fp32 [N, tokens, Hkv, D]."""
+    c = s["case"]
+    t = s["table"].long().clamp_min(0)
+    v = _values_of(codes[t], c["fmt"])
+    w = scales[t].repeat_interleave(c["block"], dim=2)
+    return (v * w[..., None]).flatten(1, 2)
+
+
+def _decode(s):
+    c = s["case"]
+    if own:
+        import attention_online_softmax_fwd_b200 as ab
+        return ab.decode_paged_q8(s["q"], s["kc"], s["vc"], s["ks"], s["vs"], s["table"], s["lens"])
+    N, Hkv, D = c["N"], c["Hkv"], c["D"]
+    k, v = _gather(s, s["kc"], s["ks"]), _gather(s, s["vc"], s["vs"])
+    q = s["q"].float().view(N, Hkv, -1, D) / math.sqrt(D)
+    score = q @ k.permute(0, 2, 3, 1)                                           # [N, Hkv, G, tokens]
+    unseen = torch.arange(k.shape[1], device=k.device)[None, :] >= s["lens"][:, None]
+    score = score.masked_fill(unseen[:, None, None, :], -math.inf)
+    m = score.amax(-1, keepdim=True)
+    m = torch.where(m == -math.inf, torch.zeros_like(m), m)                     # a sequence without tokens
+    p = torch.exp(score - m)
+    l = p.sum(-1, keepdim=True)
+    o = (p @ v.permute(0, 2, 1, 3)) / torch.where(l > 0, l, torch.ones_like(l))
+    return o.reshape(N, -1, D).to(torch.bfloat16), (m + torch.log(l)).reshape(N, -1)
+
+
+def _prefill(s):
+    c = s["case"]
+    if own:
+        import attention_online_softmax_fwd_b200 as ab
+        return ab.prefill_paged_q8(s["q"], s["kc"], s["vc"], s["ks"], s["vs"], s["table"], s["lens"])
+    N, Sq, Hq, Hkv, D = c["N"], c["Sq"], c["Hq"], c["Hkv"], c["D"]
+    k, v = _gather(s, s["kc"], s["ks"]), _gather(s, s["vc"], s["vs"])
+    q = s["q"].float().view(N, Sq, Hkv, -1, D).permute(0, 2, 3, 1, 4) / math.sqrt(D)   # [N, Hkv, G, Sq, D]
+    score = q @ k.permute(0, 2, 3, 1)[:, :, None]
+    last = s["lens"][:, None] - Sq + torch.arange(Sq, device=k.device)[None, :]
+    unseen = torch.arange(k.shape[1], device=k.device)[None, None, :] > last[:, :, None]
+    score = score.masked_fill(unseen[:, None, None], -math.inf)
+    m = score.amax(-1, keepdim=True)
+    p = torch.exp(score - m)
+    l = p.sum(-1, keepdim=True)
+    o = (p @ v.permute(0, 2, 1, 3)[:, :, None]) / l
+    o = o.permute(0, 3, 1, 2, 4).reshape(N, Sq, Hq, D).to(torch.bfloat16)
+    return o, (m + torch.log(l)).reshape(N, Hq, Sq)
+
+
+def _append(s):
+    c = s["case"]
+    if own:
+        import attention_online_softmax_fwd_b200 as ab
+        ab.kv_append_q8(s["k_new"], s["v_new"], s["kc"], s["vc"], s["ks"], s["vs"], s["table"], s["lens"])
+    else:
+        _append_plain(s, s["k_new"], s["kc"], s["ks"])
+        _append_plain(s, s["v_new"], s["vc"], s["vs"])
+    # E4M3 codes are returned as the numbers they stand for
+    as_is = (lambda t: t.view(torch.float8_e4m3fn)) if c["fmt"] == "e4m3" else (lambda t: t)
+    return dict(k=as_is(s["kc"]), v=as_is(s["vc"]), ks=s["ks"], vs=s["vs"])
+
+
+def _append_plain(s, new, codes, scales):
+    c = s["case"]
+    N, T, page, block, fmt = c["N"], c["T"], c["page"], c["block"], c["fmt"]
+    blocks = (T + 2 * block - 2) // block                                        # touched at most
+    off = s["lens"].long() % block
+    slot = torch.arange(blocks * block, device=new.device)[None, :]              # from the first touched block's start
+    fresh = (slot >= off[:, None]) & (slot < (off + T)[:, None])
+    x = new.float()[torch.arange(N, device=new.device)[:, None], (slot - off[:, None]).clamp(0, T - 1)]
+    x = torch.where(fresh[:, :, None, None], x, torch.zeros_like(x)).view(N, blocks, block, *new.shape[2:])
+    pos = (s["lens"].long() - off)[:, None] + slot
+    logical = (pos // page).clamp_max(s["table"].shape[1] - 1)
+    phys = torch.gather(s["table"].long(), 1, logical).clamp_min(0)              # [N, slots]
+    first, inner = phys[:, ::block], (pos % page // block)[:, ::block]           # [N, blocks]
+    cand = _scale_of(x.abs().amax(dim=(2, 4)), fmt)                              # [N, blocks, Hkv]
+    before = scales[first, inner]
+    holds = (torch.arange(blocks, device=new.device)[None, :] == 0) & (off > 0)[:, None]
+    scale = torch.where(holds[:, :, None], torch.maximum(before, cand), cand)
+    old = _values_of(codes[phys, pos % page], fmt).view_as(x) * before[:, :, None, :, None]
+    stays = (slot < off[:, None]).view(N, blocks, block, 1, 1)
+    q = _codes_of(torch.where(stays, old, x), scale[:, :, None, :, None], fmt).flatten(1, 2)
+    w = slot < (off + T)[:, None]
+    codes[phys[w], (pos % page)[w]] = q[w]
+    t = fresh.view(N, blocks, block).any(-1)
+    scales[first[t], inner[t]] = scale[t]
+
+
+def _read(s):
+    if own:
+        import attention_online_softmax_fwd_b200 as ab
+        return ab.kv_read_q8(s["kc"], s["vc"], s["ks"], s["vs"], s["table"], s["lens"], k_out=s["k_out"],
+                             v_out=s["v_out"])
+    T = s["k_out"].shape[1]
+    held = (torch.arange(T, device=s["k_out"].device)[None, :] < s["lens"][:, None])[:, :, None, None]
+    for codes, scales, out in ((s["kc"], s["ks"], s["k_out"]), (s["vc"], s["vs"], s["v_out"])):
+        out.copy_(torch.where(held, _gather(s, codes, scales)[:, :T].to(torch.bfloat16), out))
+    return s["k_out"], s["v_out"]
+
+
+# ------------------------------------------------------------------ what a pass cannot do without
+
+def work(case):
+    c, lens = case, _lens(case)
+    Hkv, D = c["Hkv"], c["D"]
+    held = sum(lens)
+    scales = 8 * Hkv * sum(-(-L // c["block"]) for L in lens)                    # K and V, 4 bytes each
+    table = 4 * sum(-(-L // c["page"]) for L in lens) + 4 * c["N"]
+    if c["op"] == "append":
+        new = c["N"] * c["T"] * Hkv * D
+        touched = sum((L + c["T"] - 1) // c["block"] - L // c["block"] + 1 for L in lens)
+        return {"bytes": 2 * new * 3 + 8 * Hkv * touched, "flops": 2 * new}
+    if c["op"] == "read":
+        return {"bytes": 2 * held * Hkv * D * 3 + scales + table, "flops": 2 * held * Hkv * D}
+    rows = c["N"] * c["Hq"] * c.get("Sq", 1)
+    cache = 2 * held * Hkv * D + scales + table
+    if c["op"] == "decode":
+        return {"bytes": cache + rows * (4 * D + 4), "flops": 4 * held * c["Hq"] * D}
+    pairs = sum(c["Sq"] * L - c["Sq"] * (c["Sq"] - 1) // 2 for L in lens)
+    return {"bytes": cache + rows * (4 * D + 4), "flops": 4 * pairs * c["Hq"] * D}
+
+
+# ------------------------------------------------------------------ the definition in 64 bits
+
+def _e4m3_table(dev):
+    """The 256 E4M3 values: sign, four exponent bits of bias 7, three mantissa bits."""
+    out = []
+    for b in range(256):
+        e, m = (b >> 3) & 15, b & 7
+        v = m * 2.0 ** -9 if e == 0 else (8 + m) * 2.0 ** (e - 10)
+        out.append((-v if b & 128 else v) if (b & 127) != 127 else math.nan)
+    return torch.tensor(out, dtype=torch.float64, device=dev)
+
+
+def _cached(s, codes, scales, b, L, lut):
+    """Sequence b's L cached values in 64 bits, token after token of its pages: [L, Hkv, D]."""
+    c = s["case"]
+    ids = s["table"][b, : -(-L // c["page"])].long()
+    code = codes[ids].reshape(-1, c["Hkv"], c["D"])[:L]
+    val = lut[code.long()] if c["fmt"] == "e4m3" else code.double()
+    sc = scales[ids].reshape(-1, c["Hkv"])
+    return val * sc[torch.arange(L, device=sc.device) // c["block"]].double()[:, :, None]
+
+
+def _pow2(e):
+    """2 ** e in 64 bits, exactly."""
+    return ((e.long() + 1023) << 52).view(torch.float64)
+
+
+def _round_code(x, fmt):
+    """x as the nearest code value, ties to even."""
+    if fmt == "int8":
+        return x.round().clamp(-127, 127)
+    step = _pow2(torch.frexp(x.abs())[1].clamp_min(-5) - 4)                      # an eighth of the value's binade
+    return ((x / step).round() * step).clamp(-448, 448)
+
+
+def exact(case, seed):
+    c, s = case, prepare(case, seed)
+    dev = s["table"].device
+    lut = _e4m3_table(dev)
+    lens = _lens(c)
+    Hkv, D = c["Hkv"], c["D"]
+    if c["op"] == "read":
+        outs = [t.double() for t in (s["k_out"], s["v_out"])]
+        for b, L in enumerate(lens):
+            outs[0][b, :L] = _cached(s, s["kc"], s["ks"], b, L, lut)
+            outs[1][b, :L] = _cached(s, s["vc"], s["vs"], b, L, lut)
+        return tuple(outs)
+    if c["op"] == "append":
+        got = {}
+        for name, new, codes, scales in (("k", s["k_new"], s["kc"], s["ks"]), ("v", s["v_new"], s["vc"], s["vs"])):
+            val = lut[codes.long()] if c["fmt"] == "e4m3" else codes.double()
+            sc = scales.double()
+            if c["N"] * c["T"] // c["block"] > 20000:
+                return None
+            for b, L in enumerate(lens):
+                at = L
+                while at < L + c["T"]:
+                    end = min(L + c["T"], (at // c["block"] + 1) * c["block"])
+                    page, i0 = int(s["table"][b, at // c["page"]]), at % c["page"] // c["block"] * c["block"]
+                    blk, x = i0 // c["block"], new[b, at - L:end - L].double()
+                    amax = x.abs().amax(dim=(0, 2)).clamp_min(1e-45)
+                    scale = _pow2(torch.ceil(torch.log2(amax / QMAX[c["fmt"]]) - 1e-12).clamp_min(SCALE_MIN))
+                    o = at % c["block"]
+                    if o:
+                        scale = torch.maximum(scale, sc[page, blk])
+                        v = val[page, i0:i0 + o]
+                        val[page, i0:i0 + o] = _round_code(v * (sc[page, blk] / scale)[None, :, None], c["fmt"])
+                    val[page, i0 + o:i0 + o + end - at] = _round_code(x / scale[None, :, None], c["fmt"])
+                    sc[page, blk] = scale
+                    at = end
+            got[name], got[name + "s"] = (val if c["fmt"] == "e4m3" else None), sc
+        return got
+    G = c["Hq"] // Hkv
+    Sq = c.get("Sq", 1)
+    q = s["q"].double().view(c["N"], Sq, Hkv, G, D)
+    o = torch.zeros(c["N"], Sq, Hkv, G, D, dtype=torch.float64, device=dev)
+    lse = torch.full((c["N"], Hkv, G, Sq), -math.inf, dtype=torch.float64, device=dev)
+    for b, L in enumerate(lens):
+        if L == 0:
+            continue
+        k, v = _cached(s, s["kc"], s["ks"], b, L, lut), _cached(s, s["vc"], s["vs"], b, L, lut)
+        for h in range(Hkv):
+            z = q[b, :, h].transpose(0, 1) @ k[:, h].T / math.sqrt(D)            # [G, Sq, L]
+            if c["op"] == "prefill":
+                row = torch.arange(Sq, device=dev)[:, None] + (L - Sq)
+                z = z.masked_fill(torch.arange(L, device=dev)[None, :] > row, -math.inf)
+            lse[b, h] = torch.logsumexp(z, -1)
+            o[b, :, h] = (torch.softmax(z, -1) @ v[:, h]).transpose(0, 1)
+    if c["op"] == "decode":
+        return o.reshape(c["N"], c["Hq"], D), lse.reshape(c["N"], c["Hq"])
+    return o.reshape(c["N"], Sq, c["Hq"], D), lse.reshape(c["N"], c["Hq"], Sq)
