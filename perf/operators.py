@@ -14,8 +14,9 @@ own = False
 
 #: largest code value of each format
 QMAX = {"e4m3": 448.0, "int8": 127.0}
-#: scales are at least 2 ** SCALE_MIN
+#: scales are 2 ** SCALE_MIN to 2 ** SCALE_MAX: every code times a scale is finite
 SCALE_MIN = -100
+SCALE_MAX = {"e4m3": 119, "int8": 121}
 
 
 # ------------------------------------------------------------------ cases
@@ -118,10 +119,10 @@ def _values_of(codes, fmt):
 
 
 def _scale_of(amax, fmt):
-    """The smallest power of two s with amax <= QMAX * s, at least 2 ** SCALE_MIN."""
+    """The smallest power of two s with amax <= QMAX * s, from 2 ** SCALE_MIN to 2 ** SCALE_MAX."""
     m, e = torch.frexp(amax)
     top, te = math.frexp(QMAX[fmt])
-    e = torch.where(amax > 0, e - te + (m > top).to(e.dtype), SCALE_MIN).clamp_min(SCALE_MIN)
+    e = torch.where(amax > 0, e - te + (m > top).to(e.dtype), SCALE_MIN).clamp(SCALE_MIN, SCALE_MAX[fmt])
     return ((e + 127) << 23).view(torch.float32)                                # 2 ** e, exactly
 
 
@@ -353,7 +354,8 @@ def exact(case, seed):
                     page, i0 = int(s["table"][b, at // c["page"]]), at % c["page"] // c["block"] * c["block"]
                     blk, x = i0 // c["block"], new[b, at - L:end - L].double()
                     amax = x.abs().amax(dim=(0, 2)).clamp_min(1e-45)
-                    scale = _pow2(torch.ceil(torch.log2(amax / QMAX[c["fmt"]]) - 1e-12).clamp_min(SCALE_MIN))
+                    scale = _pow2(torch.ceil(torch.log2(amax / QMAX[c["fmt"]]) - 1e-12)
+                                  .clamp(SCALE_MIN, SCALE_MAX[c["fmt"]]))
                     o = at % c["block"]
                     if o:
                         scale = torch.maximum(scale, sc[page, blk])
