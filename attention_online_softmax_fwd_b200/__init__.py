@@ -8,5 +8,6 @@ synthetic workloads.
 
 from .binding import (  # noqa: F401
     AttnError, decode_paged, decode_paged_blasst, decode_workspace_bytes, lib_path,
-    decode_paged_fp8, kv_append, load_library, prefill, prefill_blasst, prefill_paged,
+    decode_paged_fp8, decode_paged_q8, kv_append, kv_append_q8, kv_read_q8, load_library, prefill, prefill_blasst,
+    prefill_paged, prefill_paged_q8,
 )

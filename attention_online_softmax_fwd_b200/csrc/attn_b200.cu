@@ -14,7 +14,9 @@
 #include "decode_heads.cuh"
 #include "decode_blasst.cuh"
 #include "decode_gate.cuh"
+#include "decode_q8.cuh"
 #include "kv_append.cuh"
+#include "kv_q8.cuh"
 #include "prefill.cuh"
 
 using namespace attn;
@@ -543,6 +545,114 @@ int dispatch_decode_heads_fp8(int G, int hg, const CUtensorMap& tk, const CUtens
   }
 }
 
+// ------------------------------------------------------------------ 8-bit cache with block scales
+
+int log2_of(int v) {
+  int s = 0;
+  while ((1 << s) < v) ++s;
+  return s;
+}
+
+// Format, page and block sizes of an 8-bit pool. The block is a power of two from 16 up to the page.
+bool valid_q8_format(int format) { return format == ATTN_KV_E4M3 || format == ATTN_KV_INT8; }
+bool valid_q8_block(int block, int page_size) {
+  return valid_page_size(page_size) && valid_page_size(block) && block <= page_size;
+}
+
+template <int D, int GP, bool I8>
+int launch_decode_q8(const CUtensorMap& tk, const CUtensorMap& tv, const DecodeQ8Params& qp, int* ticket_counter,
+                     int sms, cudaStream_t stream) {
+  using L = DecodeQ8Smem<D, GP, I8>;
+  if (int st = set_smem_once<decode_q8_kernel<D, GP, I8>>(L::kDynamic)) return st;
+  const long long items = (long long)qp.d.max_splits * qp.d.num_seqs * qp.d.Hkv;
+  const long long slots = (long long)sms * L::kBlocks;
+  DecodeQ8Params pk = qp;
+  pk.d.static_items = items <= slots ? 1 : 0;   // one item per CTA: no ticket counter to zero
+  if (!pk.d.static_items && cudaMemsetAsync(ticket_counter, 0, sizeof(int), stream) != cudaSuccess)
+    return ATTN_ERR_CUDA;
+  decode_q8_kernel<D, GP, I8><<<dim3(unsigned(items < slots ? items : slots)), dim3(kQ8Threads), L::kDynamic,
+                                stream>>>(tk, tv, pk, ticket_counter);
+  if (int st = launch_status()) return st;
+  return launch_merge<D>(qp.d, stream);
+}
+
+// The digits of up to GP query heads are the columns of the products: the next power of two of G.
+template <int D, bool I8>
+int dispatch_decode_q8(const CUtensorMap& tk, const CUtensorMap& tv, const DecodeQ8Params& qp, int* ticket_counter,
+                       int sms, cudaStream_t s) {
+  if (qp.G == 1) return launch_decode_q8<D, 1, I8>(tk, tv, qp, ticket_counter, sms, s);
+  if (qp.G == 2) return launch_decode_q8<D, 2, I8>(tk, tv, qp, ticket_counter, sms, s);
+  if (qp.G <= 4) return launch_decode_q8<D, 4, I8>(tk, tv, qp, ticket_counter, sms, s);
+  if (qp.G <= 8) return launch_decode_q8<D, 8, I8>(tk, tv, qp, ticket_counter, sms, s);
+  return launch_decode_q8<D, 16, I8>(tk, tv, qp, ticket_counter, sms, s);
+}
+
+template <int D, bool I8>
+int launch_append_q8(const KvAppendQ8Params& p, int block, int sms, cudaStream_t stream) {
+  const int per_cta = 8 / p.warps_per_unit;
+  const long long units = (long long)p.N * p.blocks * 2 * p.Hkv;
+  long long ctas = (units + per_cta - 1) / per_cta;
+  if (ctas > (long long)sms * 16) ctas = (long long)sms * 16;
+  if (block == 256)
+    kv_append_q8_kernel<D, I8, 2><<<dim3(unsigned(ctas)), dim3(256), 0, stream>>>(p);
+  else
+    kv_append_q8_kernel<D, I8, 1><<<dim3(unsigned(ctas)), dim3(256), 0, stream>>>(p);
+  return launch_status();
+}
+
+int launch_read_q8(int format, int D, KvReadQ8Params& p, int sms, cudaStream_t stream) {
+  // about eight CTAs of eight rows per SM over all sequences, at least one for each
+  long long per = ((long long)sms * 8 + p.N - 1) / p.N;
+  const long long rows = ((long long)p.T + 7) / 8;
+  if (per > rows) per = rows;
+  p.ctas_per_seq = int(per);
+  const dim3 grid(unsigned((long long)p.N * per)), cta(256);
+  if (format == ATTN_KV_INT8) {
+    if (D == 128) kv_read_q8_kernel<128, true><<<grid, cta, 0, stream>>>(p);
+    else kv_read_q8_kernel<64, true><<<grid, cta, 0, stream>>>(p);
+  } else {
+    if (D == 128) kv_read_q8_kernel<128, false><<<grid, cta, 0, stream>>>(p);
+    else kv_read_q8_kernel<64, false><<<grid, cta, 0, stream>>>(p);
+  }
+  return launch_status();
+}
+
+// The checks that every entry point over an 8-bit pool shares (sizes and pointers).
+int check_q8_pool(const void* k_codes, const void* v_codes, const float* k_scales, const float* v_scales,
+                  const int32_t* block_table, const int32_t* lens, int format, int num_seqs, int Hkv, int D,
+                  int page_size, int scale_block, int max_pages_per_seq, int num_pages) {
+  if (!k_codes || !v_codes || !k_scales || !v_scales || !block_table || !lens) return ATTN_ERR_INVALID_ARG;
+  if (!aligned16(k_codes) || !aligned16(v_codes)) return ATTN_ERR_INVALID_ARG;
+  if (!aligned4(k_scales) || !aligned4(v_scales) || !aligned4(block_table) || !aligned4(lens))
+    return ATTN_ERR_INVALID_ARG;
+  if (!valid_q8_format(format) || num_seqs < 1 || Hkv < 1) return ATTN_ERR_INVALID_ARG;
+  if (D != 64 && D != 128) return ATTN_ERR_UNSUPPORTED;
+  if (!valid_q8_block(scale_block, page_size) || max_pages_per_seq < 1 || num_pages < 1) return ATTN_ERR_INVALID_ARG;
+  if ((long long)max_pages_per_seq * page_size > (1ll << 30)) return ATTN_ERR_INVALID_ARG;
+  if ((long long)Hkv * D > (1ll << 20)) return ATTN_ERR_UNSUPPORTED;
+  return ATTN_OK;
+}
+
+// Workspace of the prefill over an 8-bit cache, parts 256-byte aligned:
+// [block table of the scratch pages][K pages, bf16][V pages, bf16], num_seqs * max_pages pages each.
+struct PrefillQ8Layout {
+  size_t k_off = 0, v_off = 0, total = 0;
+};
+bool prefill_q8_layout(int num_seqs, int Hkv, int D, int page_size, int max_pages, PrefillQ8Layout* L) {
+  if (num_seqs < 1 || Hkv < 1 || (D != 64 && D != 128) || !valid_page_size(page_size) || max_pages < 1) return false;
+  if ((long long)num_seqs * max_pages > 0x7fffffffll) return false;
+  const size_t pages = size_t(num_seqs) * size_t(max_pages);
+  size_t pool = 0, k_off = 0, v_off = 0, end = 0;
+  if (!mul_size(pages, size_t(page_size) * size_t(D) * 2, &pool) || !mul_size(pool, size_t(Hkv), &pool)) return false;
+  if (!add_size(pages * sizeof(int32_t), 255, &k_off)) return false;
+  k_off = k_off / 256 * 256;
+  if (!add_size(k_off, pool, &v_off) || !add_size(v_off, 255, &v_off)) return false;
+  v_off = v_off / 256 * 256;
+  if (!add_size(v_off, pool, &end)) return false;
+  L->k_off = k_off; L->v_off = v_off; L->total = end;
+  return true;
+}
+
 }  // namespace
 
 extern "C" {
@@ -916,6 +1026,194 @@ int attn_decode_paged_fp8(const void* q, const void* k_codes, const void* v_code
     return st;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   return dispatch_decode_heads_fp8(G, hg, hk, hv, p, ticket_counter, sms, s);
+}
+
+int attn_kv_append_q8(const void* k_new, const void* v_new, void* k_codes, void* v_codes, float* k_scales,
+                      float* v_scales, const int32_t* block_table, const int32_t* start_pos, int format, int num_seqs,
+                      int T, int Hkv, int D, int page_size, int scale_block, int max_pages_per_seq, int num_pages,
+                      int* device_status, void* stream) {
+  if (!k_new || !v_new || !aligned16(k_new) || !aligned16(v_new)) return ATTN_ERR_INVALID_ARG;
+  if (int st = check_q8_pool(k_codes, v_codes, k_scales, v_scales, block_table, start_pos, format, num_seqs, Hkv, D,
+                             page_size, scale_block, max_pages_per_seq, num_pages))
+    return st;
+  if (T < 1 || T > (1 << 30)) return ATTN_ERR_INVALID_ARG;
+  int sms = 0;
+  if (int st = current_device(&sms)) return st;
+  KvAppendQ8Params p{};
+  p.k_new = static_cast<const __nv_bfloat16*>(k_new);
+  p.v_new = static_cast<const __nv_bfloat16*>(v_new);
+  p.k_codes = static_cast<uint8_t*>(k_codes);
+  p.v_codes = static_cast<uint8_t*>(v_codes);
+  p.k_scales = k_scales;
+  p.v_scales = v_scales;
+  p.block_table = block_table;
+  p.start_pos = start_pos;
+  p.status = device_status;
+  p.N = num_seqs; p.T = T; p.Hkv = Hkv;
+  p.max_pages = max_pages_per_seq; p.num_pages = num_pages;
+  p.page_shift = log2_of(page_size);
+  p.block_shift = log2_of(scale_block);
+  p.blocks = int(((long long)T + 2ll * scale_block - 2) / scale_block);
+  p.warps_per_unit = scale_block / 16 < 8 ? scale_block / 16 : 8;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  if (format == ATTN_KV_INT8)
+    return D == 128 ? launch_append_q8<128, true>(p, scale_block, sms, s)
+                    : launch_append_q8<64, true>(p, scale_block, sms, s);
+  return D == 128 ? launch_append_q8<128, false>(p, scale_block, sms, s)
+                  : launch_append_q8<64, false>(p, scale_block, sms, s);
+}
+
+int attn_kv_read_q8(const void* k_codes, const void* v_codes, const float* k_scales, const float* v_scales,
+                    const int32_t* block_table, const int32_t* seq_lens, void* k_out, void* v_out, int format,
+                    int num_seqs, int T, int Hkv, int D, int page_size, int scale_block, int max_pages_per_seq,
+                    int num_pages, int* device_status, void* stream) {
+  if (!k_out || !v_out || !aligned16(k_out) || !aligned16(v_out)) return ATTN_ERR_INVALID_ARG;
+  if (int st = check_q8_pool(k_codes, v_codes, k_scales, v_scales, block_table, seq_lens, format, num_seqs, Hkv, D,
+                             page_size, scale_block, max_pages_per_seq, num_pages))
+    return st;
+  if (T < 1 || (long long)T > (long long)max_pages_per_seq * page_size) return ATTN_ERR_INVALID_ARG;
+  int sms = 0;
+  if (int st = current_device(&sms)) return st;
+  KvReadQ8Params p{};
+  p.k_codes = static_cast<const uint8_t*>(k_codes);
+  p.v_codes = static_cast<const uint8_t*>(v_codes);
+  p.k_scales = k_scales;
+  p.v_scales = v_scales;
+  p.block_table = block_table;
+  p.seq_lens = seq_lens;
+  p.k_out = static_cast<__nv_bfloat16*>(k_out);
+  p.v_out = static_cast<__nv_bfloat16*>(v_out);
+  p.status = device_status;
+  p.N = num_seqs; p.T = T; p.Hkv = Hkv;
+  p.max_pages = max_pages_per_seq; p.num_pages = num_pages;
+  p.page_shift = log2_of(page_size);
+  p.block_shift = log2_of(scale_block);
+  return launch_read_q8(format, D, p, sms, static_cast<cudaStream_t>(stream));
+}
+
+int attn_decode_q8_split_tokens(int num_seqs, int Hkv, int max_pages_per_seq, int page_size) {
+  if (num_seqs < 1 || Hkv < 1 || max_pages_per_seq < 1 || !valid_page_size(page_size)) return 0;
+  const long long cap = (long long)max_pages_per_seq * page_size;
+  if (cap > (1ll << 30)) return 0;
+  // two CTAs on each of the 148 SMs: one item for each while that leaves at most 1024 tokens to an item,
+  // items of 1024 tokens beyond
+  const long long per = (long long)num_seqs * Hkv * ((cap + kQ8Tok - 1) / kQ8Tok);   // tiles, at most
+  long long split = (per + 295) / 296 * kQ8Tok;
+  if (split > 1024) split = 1024;
+  return int(split);
+}
+
+int attn_decode_paged_q8(const void* q, const void* k_codes, const void* v_codes, const float* k_scales,
+                         const float* v_scales, const int32_t* block_table, const int32_t* seq_lens, int format,
+                         int num_seqs, int Hq, int Hkv, int D, int page_size, int scale_block, int max_pages_per_seq,
+                         int num_pages, float scale, int split_tokens, void* o, float* lse, void* workspace,
+                         size_t workspace_bytes, int* device_status, void* stream) {
+  if (!q || !o || !workspace || !aligned16(q) || !aligned16(o) || !aligned16(workspace) || !aligned4(lse))
+    return ATTN_ERR_INVALID_ARG;
+  if (int st = check_q8_pool(k_codes, v_codes, k_scales, v_scales, block_table, seq_lens, format, num_seqs, Hkv, D,
+                             page_size, scale_block, max_pages_per_seq, num_pages))
+    return st;
+  if (Hq < 1 || Hq % Hkv != 0) return ATTN_ERR_INVALID_ARG;
+  // merge CTAs: one per (sequence, head), or one per 32 of its head dimensions
+  if ((long long)num_seqs * Hq * (D / 32) > 0x7fffffffll) return ATTN_ERR_INVALID_ARG;
+  if (split_tokens < 64 || split_tokens % 64 != 0) return ATTN_ERR_INVALID_ARG;
+  if (!std::isfinite(scale) || !(scale > 0.f)) return ATTN_ERR_INVALID_ARG;
+  const int G = Hq / Hkv;
+  if (G > 16) return ATTN_ERR_UNSUPPORTED;
+  const size_t need = attn_decode_workspace_bytes(num_seqs, Hq, D, max_pages_per_seq, page_size, split_tokens);
+  if (need == 0 || workspace_bytes < need) return ATTN_ERR_INVALID_ARG;
+  int sms = 0;
+  if (int st = current_device(&sms)) return st;
+
+  DecodeQ8Params qp{};
+  DecodeParams& p = qp.d;
+  p.q = static_cast<const __nv_bfloat16*>(q);
+  p.block_table = block_table;
+  p.seq_lens = seq_lens;
+  p.o = static_cast<__nv_bfloat16*>(o);
+  p.lse = lse;
+  const long long ms = max_splits_of(max_pages_per_seq, page_size, split_tokens);
+  int* ticket_counter = static_cast<int*>(workspace);
+  p.ws_o = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + kWsHeader);
+  size_t o_bytes = 0;
+  decode_ws_bytes(size_t(num_seqs) * size_t(ms), size_t(Hq), size_t(D), &o_bytes);   // checked above
+  p.ws_lse = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + kWsHeader + (o_bytes + 255) / 256 * 256);
+  p.status = device_status;
+  p.num_seqs = num_seqs; p.Hq = Hq; p.Hkv = Hkv;
+  p.page_size = page_size; p.max_pages = max_pages_per_seq; p.num_pages = num_pages;
+  p.split_tokens = split_tokens;
+  p.max_splits = int(ms);
+  p.scale_log2 = scale * 1.4426950408889634f;
+  p.log2_lambda = -INFINITY;
+  qp.k_scales = k_scales;
+  qp.v_scales = v_scales;
+  qp.G = G;
+  qp.page_shift = log2_of(page_size);
+  qp.block_shift = log2_of(scale_block);
+
+  // code pool [P][page_size][Hkv][D] as a 4-D map {D, page_size, Hkv, P}; box = 16 slots of one head,
+  // landing as 16 rows of D bytes under the swizzle of that width
+  const uint64_t dims[4] = {uint64_t(D), uint64_t(page_size), uint64_t(Hkv), uint64_t(num_pages)};
+  const uint64_t strides[3] = {uint64_t(Hkv) * D, uint64_t(D), uint64_t(page_size) * Hkv * D};
+  const uint32_t box[4] = {uint32_t(D), uint32_t(kQ8Chunk), 1, 1};
+  const CUtensorMapSwizzle swizzle = D == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B;
+  CUtensorMap tk, tv;
+  if (int st = encode_map(&tk, k_codes, dims, strides, box, swizzle, CU_TENSOR_MAP_DATA_TYPE_UINT8)) return st;
+  if (int st = encode_map(&tv, v_codes, dims, strides, box, swizzle, CU_TENSOR_MAP_DATA_TYPE_UINT8)) return st;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  if (format == ATTN_KV_INT8)
+    return D == 128 ? dispatch_decode_q8<128, true>(tk, tv, qp, ticket_counter, sms, s)
+                    : dispatch_decode_q8<64, true>(tk, tv, qp, ticket_counter, sms, s);
+  return D == 128 ? dispatch_decode_q8<128, false>(tk, tv, qp, ticket_counter, sms, s)
+                  : dispatch_decode_q8<64, false>(tk, tv, qp, ticket_counter, sms, s);
+}
+
+size_t attn_prefill_paged_q8_workspace_bytes(int num_seqs, int Hkv, int D, int max_pages_per_seq, int page_size) {
+  PrefillQ8Layout L;
+  return prefill_q8_layout(num_seqs, Hkv, D, page_size, max_pages_per_seq, &L) ? L.total : 0;
+}
+
+int attn_prefill_paged_q8(const void* q, const void* k_codes, const void* v_codes, const float* k_scales,
+                          const float* v_scales, const int32_t* block_table, const int32_t* seq_lens, void* o,
+                          float* lse, int format, int B, int Sq, int Hq, int Hkv, int D, int page_size,
+                          int scale_block, int max_pages_per_seq, int num_pages, float scale, void* workspace,
+                          size_t workspace_bytes, int* device_status, void* stream) {
+  if (!q || !o || !workspace || !aligned16(q) || !aligned16(o) || !aligned16(workspace) || !aligned4(lse))
+    return ATTN_ERR_INVALID_ARG;
+  if (int st = check_q8_pool(k_codes, v_codes, k_scales, v_scales, block_table, seq_lens, format, B, Hkv, D, page_size,
+                             scale_block, max_pages_per_seq, num_pages))
+    return st;
+  // what the prefill over the scratch pages would refuse is refused before anything is enqueued
+  if (Sq < 1 || Hq < 1 || Hq % Hkv != 0) return ATTN_ERR_INVALID_ARG;
+  if ((long long)Sq > (long long)max_pages_per_seq * page_size) return ATTN_ERR_INVALID_ARG;
+  if (!std::isfinite(scale) || !(scale > 0.f)) return ATTN_ERR_INVALID_ARG;
+  if ((long long)B * Sq * Hq > (1ll << 40)) return ATTN_ERR_INVALID_ARG;
+  if ((((long long)Sq + 2 * kPfRows - 1) / (2 * kPfRows)) * B * Hq > 0x7fffffffll) return ATTN_ERR_UNSUPPORTED;
+  PrefillQ8Layout L;
+  if (!prefill_q8_layout(B, Hkv, D, page_size, max_pages_per_seq, &L) || workspace_bytes < L.total)
+    return ATTN_ERR_INVALID_ARG;
+  int sms = 0;
+  if (int st = current_device(&sms)) return st;
+  uint8_t* ws = static_cast<uint8_t*>(workspace);
+  KvReadQ8Params p{};
+  p.k_codes = static_cast<const uint8_t*>(k_codes);
+  p.v_codes = static_cast<const uint8_t*>(v_codes);
+  p.k_scales = k_scales;
+  p.v_scales = v_scales;
+  p.block_table = block_table;
+  p.seq_lens = seq_lens;
+  p.k_out = reinterpret_cast<__nv_bfloat16*>(ws + L.k_off);
+  p.v_out = reinterpret_cast<__nv_bfloat16*>(ws + L.v_off);
+  p.identity = reinterpret_cast<int32_t*>(ws);
+  p.status = device_status;
+  p.N = B; p.T = max_pages_per_seq * page_size; p.Hkv = Hkv;
+  p.min_len = Sq;
+  p.max_pages = max_pages_per_seq; p.num_pages = num_pages;
+  p.page_shift = log2_of(page_size);
+  p.block_shift = log2_of(scale_block);
+  if (int st = launch_read_q8(format, D, p, sms, static_cast<cudaStream_t>(stream))) return st;
+  return attn_prefill_paged(q, ws + L.k_off, ws + L.v_off, p.identity, seq_lens, o, lse, B, Sq, Hq, Hkv, D, page_size,
+                            max_pages_per_seq, B * max_pages_per_seq, scale, device_status, stream);
 }
 
 }  // extern "C"

@@ -190,6 +190,25 @@ def quantize_pool_e4m3(pool):
     return codes, scale
 
 
+def quantize_pool_q8(pool, block, kind="e4m3"):
+    """Codes (uint8 E4M3 or int8) and power-of-two scales fp32 [P, page_size / block, Hkv] of a bf16 page
+    pool: per (page, block of slots, head) the smallest power of two that holds the finite values. Slots
+    whose values are not finite (unused ones of a poisoned pool) get the NaN code (int8: -128)."""
+    P, page_size, Hkv, D = pool.shape
+    qmax = 448.0 if kind == "e4m3" else 127.0
+    x = pool.float().view(P, page_size // block, block, Hkv, D)
+    fin = torch.isfinite(x)
+    amax = torch.where(fin, x, torch.zeros_like(x)).abs().amax(dim=(2, 4)).double()
+    e = torch.ceil(torch.log2(amax.clamp_min(2.0 ** -90) / qmax) - 1e-12)
+    scales = torch.exp2(e).float()
+    y = x / scales[:, :, None, :, None]
+    if kind == "e4m3":
+        codes = y.to(torch.float8_e4m3fn).view(torch.uint8)
+    else:
+        codes = torch.where(fin, torch.round(y), torch.full_like(y, -128.0)).to(torch.int8)
+    return codes.view(P, page_size, Hkv, D).contiguous(), scales.contiguous()
+
+
 # The workloads the library is measured and checked on (sizes as named).
 CONFIGS = {
     "tiny_gqa_prefill": dict(kind="prefill", B=1, Hq=4, Hkv=2, S=128, D=64, causal=True, seed=1001),

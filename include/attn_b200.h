@@ -316,6 +316,113 @@ int attn_decode_paged_fp8(const void* q, const void* k_codes, const void* v_code
                           int* device_status, void* stream);
 
 /*
+ * ---- 8-bit paged cache with a scale for each block of tokens and head ----
+ *
+ * The TensorRT-LLM page ("TensorRT-LLM：大模型推理优化利器", section 量化) names
+ * low-precision formats that cut the cache's memory and bandwidth; how the codes
+ * are scaled is this library's reading. A cached value is scale * code:
+ *   codes   [num_pages][page_size][Hkv][D], one byte each: `format` says whether
+ *           they are E4M3 (as at attn_decode_paged_fp8) or int8 integers
+ *   scales  [num_pages][page_size / scale_block][Hkv] fp32: slots
+ *           [i * scale_block, (i + 1) * scale_block) of a page share scale i of
+ *           their head. Finite and >= 0; any such value is read, the library
+ *           writes powers of two. A NaN (or negative V) scale makes its block
+ *           read as NaN: results that see the block are NaN.
+ *   scale_block  16, 32, 64, 128 or 256, at most page_size
+ * Four entry points make a serving loop: attn_kv_append_q8 writes new tokens,
+ * attn_decode_paged_q8 and attn_prefill_paged_q8 attend over the cache,
+ * attn_kv_read_q8 widens it to bf16. Page sizes, block tables, lengths,
+ * D (64 or 128), status codes and stream behaviour are those of the bf16 cache;
+ * codes, q and o are 16-byte aligned, scales, tables and lengths 4-byte aligned,
+ * Hkv * D at most 2^20.
+ */
+enum attn_kv_format {
+  ATTN_KV_E4M3 = 0,  /* FP8 E4M3 codes, |code| <= 448                              */
+  ATTN_KV_INT8 = 1   /* signed bytes; the library writes -127 .. 127, reads -128 too */
+};
+
+/*
+ * attn_kv_append_q8 -- quantise the keys and values of new tokens into the pages.
+ * Arguments and positions as attn_kv_append, with codes and scales for the pages.
+ * For each block of tokens and head that new tokens enter:
+ *   c = the smallest power of two >= 2^-100 with max |x| <= Q c over the block's
+ *       new tokens (Q = 448 for E4M3, 127 for int8), at most 2^119 or 2^121 so
+ *       that every code reads as a finite number (values beyond saturate)
+ *   the block's first slot is new: its scale becomes c, whatever it was
+ *   tokens sit before the new ones: s' = max(s, c); if s' > s the earlier codes
+ *       are rounded again, code' = round(code * s / s')
+ *   new codes = round(x / s'), to nearest, ties to even
+ * Slots of the block past the new tokens keep their codes (they hold nothing).
+ * A NaN or an infinity among the new tokens makes the block's scale NaN, until
+ * the block is written again from its first slot.
+ * A block that receives tokens must belong to one sequence: pages that sequences
+ * share may be read by all of them, but a call that writes into the same block
+ * for two sequences is undefined. Positions past the table, or pages outside the
+ * pool, are skipped and ATTN_ERR_DEVICE_BOUNDS set. Calling again with the same
+ * arguments changes nothing.
+ */
+int attn_kv_append_q8(const void* k_new, const void* v_new, void* k_codes, void* v_codes, float* k_scales,
+                      float* v_scales, const int32_t* block_table, const int32_t* start_pos, int format,
+                      int num_seqs, int T, int Hkv, int D, int page_size, int scale_block, int max_pages_per_seq,
+                      int num_pages, int* device_status, void* stream);
+
+/*
+ * attn_kv_read_q8 -- read the first tokens of each sequence back as bf16.
+ *   k_out, v_out  [num_seqs][T][Hkv][D] bf16, 16-byte aligned: row t of sequence b
+ *                 is token t for t < min(seq_lens[b], T); other rows are left as
+ *                 they were. T <= max_pages_per_seq * page_size.
+ * scale * code is rounded to bf16 once; with scales that are powers of two, as
+ * attn_kv_append_q8 writes them, nothing is rounded. Rows of a page outside
+ * [0, num_pages) are zero and ATTN_ERR_DEVICE_BOUNDS is set, as it is for a
+ * length outside [0, max_pages_per_seq * page_size].
+ */
+int attn_kv_read_q8(const void* k_codes, const void* v_codes, const float* k_scales, const float* v_scales,
+                    const int32_t* block_table, const int32_t* seq_lens, void* k_out, void* v_out, int format,
+                    int num_seqs, int T, int Hkv, int D, int page_size, int scale_block, int max_pages_per_seq,
+                    int num_pages, int* device_status, void* stream);
+
+/*
+ * attn_decode_q8_split_tokens -- a good split_tokens for attn_decode_paged_q8 (host
+ * arithmetic only): a multiple of 128, at most 1024. 0 for invalid arguments.
+ */
+int attn_decode_q8_split_tokens(int num_seqs, int Hkv, int max_pages_per_seq, int page_size);
+
+/*
+ * attn_decode_paged_q8 -- attn_decode_paged (dense) over the 8-bit cache. The
+ * codes enter the tensor cores as they are; the scales enter the scores and the
+ * probabilities, so no widened key or value is rounded. Any Hkv; Hq / Hkv from 1
+ * to 16. q, o, lse, split_tokens, the workspace (attn_decode_workspace_bytes with
+ * the same sizes), empty sequences and bad pages are those of attn_decode_paged.
+ * q is split into two 8-bit digits scaled to its largest value: its elements
+ * below 2^-14 (E4M3) or 2^-8 (int8) of the row's largest lose their last bits
+ * (absolute error at most 2^-22 or 2^-14 of the largest). A query row with a NaN
+ * or an infinity gives a NaN output row.
+ */
+int attn_decode_paged_q8(const void* q, const void* k_codes, const void* v_codes, const float* k_scales,
+                         const float* v_scales, const int32_t* block_table, const int32_t* seq_lens, int format,
+                         int num_seqs, int Hq, int Hkv, int D, int page_size, int scale_block,
+                         int max_pages_per_seq, int num_pages, float scale, int split_tokens, void* o, float* lse,
+                         void* workspace, size_t workspace_bytes, int* device_status, void* stream);
+
+/*
+ * attn_prefill_paged_q8 -- attn_prefill_paged over the 8-bit cache: the chunk's
+ * queries see the cached keys, end-aligned and causal, the chunk's own included
+ * (append them first). The sequences' cache is widened once into bf16 pages in
+ * the workspace (as attn_kv_read_q8), which the prefill then reads: every query
+ * block and head of a group shares that one conversion. Arguments as
+ * attn_prefill_paged; the workspace (16-byte aligned, contents ignored) holds at
+ * least attn_prefill_paged_q8_workspace_bytes(...) bytes: bf16 K and V of
+ * B * max_pages_per_seq pages and a block table, so a table trimmed to the pages
+ * in use keeps it small. Returns 0 for invalid arguments or an overflowing size.
+ */
+size_t attn_prefill_paged_q8_workspace_bytes(int B, int Hkv, int D, int max_pages_per_seq, int page_size);
+int attn_prefill_paged_q8(const void* q, const void* k_codes, const void* v_codes, const float* k_scales,
+                          const float* v_scales, const int32_t* block_table, const int32_t* seq_lens, void* o,
+                          float* lse, int format, int B, int Sq, int Hq, int Hkv, int D, int page_size,
+                          int scale_block, int max_pages_per_seq, int num_pages, float scale, void* workspace,
+                          size_t workspace_bytes, int* device_status, void* stream);
+
+/*
  * attn_decode_paged_noalloc -- attn_decode_paged without a caller-provided
  * workspace. (Library plumbing: the pages describe no counterpart.)
  *

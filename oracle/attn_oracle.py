@@ -289,6 +289,118 @@ def decode_paged_fp8(q, k_codes, v_codes, k_scale: float, v_scale: float, block_
 
 
 # ----------------------------------------------------------------------------
+# 8-bit cache with one scale per block of tokens and head
+# ----------------------------------------------------------------------------
+#
+# The TensorRT-LLM page ("TensorRT-LLM：大模型推理优化利器", 量化) names the low-precision
+# formats without their scaling; the reading used: value = scale * code, codes
+# [P, page_size, Hkv, D] E4M3 (uint8) or integers (int8), scales
+# [P, page_size / block, Hkv], slots [i * block, (i + 1) * block) sharing scale i.
+
+Q8_MAX = {"uint8": 448.0, "int8": 127.0}
+Q8_MIN_SCALE = 2.0 ** -100
+Q8_MAX_SCALE = {"uint8": 2.0 ** 119, "int8": 2.0 ** 121}    # every code times a scale stays finite in fp32
+
+
+def _host(x):
+    return x.detach().cpu().numpy() if hasattr(x, "detach") else np.asarray(x)
+
+
+def q8_values(codes):
+    """Float64 values of codes: E4M3 for uint8, the integers for int8."""
+    c = _host(codes)
+    if c.dtype == np.uint8:
+        return e4m3_to_float(c)
+    if c.dtype != np.int8:
+        raise TypeError("codes are uint8 or int8")
+    return c.astype(np.float64)
+
+
+def q8_dequant(codes, scales):
+    """Float64 pool scale * code."""
+    v, s = q8_values(codes), _host(scales).astype(np.float64)
+    block = v.shape[1] // s.shape[1]
+    return v * np.repeat(s, block, axis=1)[..., None]
+
+
+def q8_block_scale(amax: float, kind: str) -> float:
+    """The smallest power of two s >= 2^-100 with amax <= Q s, at most Q8_MAX_SCALE (larger values then
+    saturate); NaN for an amax that is not finite."""
+    if not np.isfinite(amax):
+        return float("nan")
+    s = Q8_MIN_SCALE
+    while amax > Q8_MAX[kind] * s and s < Q8_MAX_SCALE[kind]:
+        s *= 2.0
+    return s
+
+
+def q8_round(x, kind: str):
+    """The nearest code of each value (ties to even), as uint8 or int8 codes."""
+    x = np.asarray(x, dtype=np.float64)
+    if kind == "int8":
+        return np.clip(np.rint(x), -127, 127).astype(np.int8)
+    mag = np.minimum(np.abs(x), 448.0)
+    e = np.clip(np.floor(np.log2(np.where(mag > 0, mag, 1.0))), -6, 8)
+    n = np.rint(mag / 2.0 ** (e - 3)).astype(np.int64)      # eighths of the binade: 0..16 (0..8 below 2^-6)
+    code = np.where(n >= 8, (e.astype(np.int64) + 7) * 8 + (n - 8), n)   # n = 16 carries into the next binade
+    return (code + np.where(np.signbit(x), 128, 0)).astype(np.uint8)
+
+
+def kv_append_q8(k_codes, v_codes, k_scales, v_scales, block_table, start_pos, k_new, v_new):
+    """Quantise new tokens into the pages; returns new (k_codes, v_codes, k_scales, v_scales).
+
+    Per (block, head) that new tokens enter: c = q8_block_scale of the new tokens'
+    largest |x|; the scale becomes c when the block's first slot is new, else
+    max(s, c), the earlier codes being rounded again to a scale that grew; new
+    codes = round(x / scale). Raises IndexError as kv_append does."""
+    out = []
+    bt, starts = np.asarray(block_table), np.asarray(start_pos)
+    for codes, scales, new in ((k_codes, k_scales, k_new), (v_codes, v_scales, v_new)):
+        c, s, x = _host(codes).copy(), _host(scales).astype(np.float64), _f64(new)
+        kind = str(c.dtype)
+        page_size, block = c.shape[1], c.shape[1] // s.shape[1]
+        for b in range(x.shape[0]):
+            pos, end = int(starts[b]), int(starts[b]) + x.shape[1]
+            while pos < end:
+                stop = min(end, (pos // block + 1) * block)
+                if pos // page_size >= bt.shape[1]:
+                    raise IndexError(f"sequence {b}: position {pos} past the block table")
+                page = int(bt[b, pos // page_size])
+                if page < 0 or page >= c.shape[0]:
+                    raise IndexError(f"sequence {b}: block_table entry {page} out of range")
+                i, kept = pos % page_size // block, pos % block
+                first = i * block
+                for h in range(c.shape[2]):
+                    rows = x[b, pos - int(starts[b]):stop - int(starts[b]), h]
+                    want = q8_block_scale(np.abs(rows).max(), kind)
+                    old = s[page, i, h]
+                    if kept and not want > old and not np.isnan(want):
+                        want = old
+                    elif kept and not np.isnan(want):
+                        was = q8_values(c[page, first:first + kept, h])
+                        c[page, first:first + kept, h] = q8_round(was * (old / want), kind)
+                    s[page, i, h] = want
+                    if np.isfinite(want):
+                        c[page, first + kept:first + kept + stop - pos, h] = q8_round(rows / want, kind)
+                pos = stop
+        out += [c, s]
+    return out[0], out[2], out[1], out[3]
+
+
+def decode_paged_q8(q, k_codes, v_codes, k_scales, v_scales, block_table, seq_lens, scale: float, seqs=None):
+    """Single-token decode over the 8-bit cache: decode_paged on the dequantised pools."""
+    k, v = q8_dequant(k_codes, k_scales), q8_dequant(v_codes, v_scales)
+    return decode_paged(q, k, v, block_table, seq_lens, k.shape[1], scale, seqs=seqs)
+
+
+def prefill_paged_q8(q, k_codes, v_codes, k_scales, v_scales, block_table, seq_lens, scale: float, seqs=None,
+                     heads=None):
+    """Chunked prefill over the 8-bit cache: prefill_paged on the dequantised pools."""
+    k, v = q8_dequant(k_codes, k_scales), q8_dequant(v_codes, v_scales)
+    return prefill_paged(q, k, v, block_table, seq_lens, k.shape[1], scale, seqs=seqs, heads=heads)
+
+
+# ----------------------------------------------------------------------------
 # BLASST walk
 # ----------------------------------------------------------------------------
 
