@@ -8,7 +8,6 @@ built, every entry point raises :class:`AttnError`; there is no fallback.
 
 from __future__ import annotations
 
-import contextlib
 import ctypes
 import math
 import os
@@ -59,8 +58,8 @@ SIGNATURES = {
                                    _P, _SZ, _P, _P]),
     "attn_kv_append_q8": (_I, [_P, _P, _P, _P, _P, _P, _P, _P, _I, _I, _I, _I, _I, _I, _I, _I, _I, _P, _P]),
     "attn_kv_read_q8": (_I, [_P, _P, _P, _P, _P, _P, _P, _P, _I, _I, _I, _I, _I, _I, _I, _I, _I, _P, _P]),
-    "attn_decode_q8_split_tokens": (_I, [_I, _I, _I, _I]),
-    "attn_decode_paged_q8": (_I, [_P, _P, _P, _P, _P, _P, _P, _I, _I, _I, _I, _I, _I, _I, _I, _I, _F, _I, _P, _P,
+    "attn_decode_paged_q8_workspace_bytes": (_SZ, [_I, _I, _I]),
+    "attn_decode_paged_q8": (_I, [_P, _P, _P, _P, _P, _P, _P, _I, _I, _I, _I, _I, _I, _I, _I, _I, _F, _P, _P,
                                   _P, _SZ, _P, _P]),
     "attn_prefill_paged_q8_workspace_bytes": (_SZ, [_I, _I, _I, _I, _I]),
     "attn_prefill_paged_q8": (_I, [_P, _P, _P, _P, _P, _P, _P, _P, _P, _I, _I, _I, _I, _I, _I, _I, _I, _I, _I, _F,
@@ -392,58 +391,74 @@ def decode_paged_noalloc(q, k_pages, v_pages, block_table, seq_lens, scale=None,
 
 KV_E4M3, KV_INT8 = 0, 1   # attn_kv_format
 
+# These calls are short (a decode step appends and attends for every layer), so their host side is kept
+# short as well: pointers go to ctypes as integers, and the checks touch each tensor once.
+_raw_stream = torch._C._cuda_getCurrentRawStream if hasattr(torch._C, "_cuda_getCurrentRawStream") \
+    else lambda dev: torch.cuda.current_stream(dev).cuda_stream
+_U8, _I8, _F32, _I32, _BF16 = torch.uint8, torch.int8, torch.float32, torch.int32, torch.bfloat16
+
 
 def _q8_pool(k_codes, v_codes, k_scales, v_scales, block_table, lens, lens_name):
-    """Checks an 8-bit paged cache; returns (format, pages, page_size, Hkv, D, tokens per scale).
+    """Checks an 8-bit paged cache; returns (format, pages, page_size, Hkv, D, tokens per scale, device index).
 
     Codes are uint8 (E4M3) or int8 [P, page_size, Hkv, D]; scales fp32 [P, page_size / block, Hkv]."""
-    if not isinstance(k_codes, torch.Tensor) or k_codes.dtype not in (torch.uint8, torch.int8):
+    named = (("k_codes", k_codes), ("v_codes", v_codes), ("k_scales", k_scales), ("v_scales", v_scales),
+             ("block_table", block_table), (lens_name, lens))
+    for name, t in named:
+        if not isinstance(t, torch.Tensor):
+            raise AttnError(f"{name}: expected a tensor")
+    kind = k_codes.dtype
+    if kind is not _U8 and kind is not _I8:
         raise AttnError("k_codes: expected uint8 (E4M3) or int8 codes")
-    _need(k_codes, k_codes.dtype, 4, "k_codes")
-    _need(v_codes, k_codes.dtype, 4, "v_codes")
-    _need(k_scales, torch.float32, 3, "k_scales")
-    _need(v_scales, torch.float32, 3, "v_scales")
-    _need(block_table, torch.int32, 2, "block_table")
-    _need(lens, torch.int32, 1, lens_name)
-    P, page_size, Hkv, D = k_codes.shape
-    blocks = k_scales.shape[1]
-    if v_codes.shape != k_codes.shape or v_scales.shape != k_scales.shape or k_scales.shape[0] != P \
-            or k_scales.shape[2] != Hkv or blocks < 1 or page_size % blocks != 0:
+    shape, sshape = k_codes.shape, k_scales.shape
+    if v_codes.dtype is not kind or k_scales.dtype is not _F32 or v_scales.dtype is not _F32 \
+            or block_table.dtype is not _I32 or lens.dtype is not _I32:
+        raise AttnError("codes must share a type, scales be float32, block_table and lengths int32")
+    if len(shape) != 4 or len(sshape) != 3 or block_table.dim() != 2 or lens.dim() != 1 or v_codes.shape != shape \
+            or v_scales.shape != sshape or sshape[0] != shape[0] or sshape[2] != shape[2] or sshape[1] < 1 \
+            or shape[1] % sshape[1] != 0:
         raise AttnError("codes must be [P, page_size, Hkv, D] and scales [P, page_size / block, Hkv]")
     if block_table.shape[0] != lens.shape[0]:
         raise AttnError(f"block_table and {lens_name} must hold one row and one entry per sequence")
-    dev = k_codes.device
-    if v_codes.device != dev or k_scales.device != dev or v_scales.device != dev or block_table.device != dev \
-            or lens.device != dev:
-        raise AttnError("the cache's tensors must be on one device")
-    return (KV_E4M3 if k_codes.dtype == torch.uint8 else KV_INT8), P, page_size, Hkv, D, page_size // blocks
+    dev = k_codes.get_device()
+    for name, t in named:
+        if not t.is_cuda or t.get_device() != dev or not t.is_contiguous():
+            raise AttnError(f"{name}: expected a contiguous CUDA tensor on the cache's device")
+    return (KV_E4M3 if kind is _U8 else KV_INT8), shape[0], shape[1], shape[2], shape[3], shape[1] // sshape[1], dev
 
 
-def _q8_like(t, dtype, shape, dev, name):
-    """Checks a caller's buffer (None passes)."""
-    if t is None:
-        return
-    _need(t, dtype, len(shape), name)
-    if t.shape != torch.Size(shape) or t.device != dev:
-        raise AttnError(f"{name}: expected shape {tuple(shape)} on {dev}")
+def _q8_buffer(t, dtype, shape, dev, name):
+    """Checks one tensor of a call: type, exact shape, device, contiguity."""
+    if not isinstance(t, torch.Tensor) or t.dtype is not dtype or t.shape != shape:
+        raise AttnError(f"{name}: expected a {dtype} tensor of shape {tuple(shape)}")
+    if not t.is_cuda or t.get_device() != dev or not t.is_contiguous():
+        raise AttnError(f"{name}: expected a contiguous CUDA tensor on the cache's device")
 
 
-def _q8_status(device_status, dev):
-    if device_status is not None and (not isinstance(device_status, torch.Tensor) or device_status.dtype != torch.int32
-                                      or device_status.numel() < 1 or device_status.device != dev):
-        raise AttnError(f"device_status: expected an int32 tensor on {dev}")
-    return _ptr(device_status)
+def _q8_scratch(workspace, need, device_status, dev):
+    """Checks an optional workspace and status word; returns the status word's address or None."""
+    if workspace is not None and (not isinstance(workspace, torch.Tensor) or not workspace.is_cuda
+                                  or not workspace.is_contiguous() or workspace.get_device() != dev
+                                  or workspace.numel() * workspace.element_size() < need):
+        raise AttnError(f"workspace: expected a contiguous tensor of at least {need} bytes on the cache's device")
+    if device_status is None:
+        return None
+    if not isinstance(device_status, torch.Tensor) or device_status.dtype is not _I32 or device_status.numel() < 1 \
+            or not device_status.is_cuda or device_status.get_device() != dev:
+        raise AttnError("device_status: expected an int32 tensor on the cache's device")
+    return device_status.data_ptr()
 
 
-def _on(dev, stream):
-    """Makes the tensors' device, and the stream that the call runs on, current: what the
-    call allocates then belongs to that stream."""
-    if stream is None and dev.index == torch.cuda.current_device():
-        return contextlib.nullcontext()
-    s = torch.cuda.current_stream(dev) if stream is None else stream
-    if s.device != dev:
-        raise AttnError(f"stream: belongs to {s.device}, the tensors are on {dev}")
-    return torch.cuda.stream(s)
+def _q8_elsewhere(dev, stream):
+    """None when the call can run on the current device and stream; otherwise the context that makes the
+    tensors' device and the stream current, so that what the call allocates belongs to that stream."""
+    if stream is None:
+        if dev == torch.cuda.current_device():
+            return None
+        return torch.cuda.stream(torch.cuda.current_stream(dev))
+    if stream.device.index != dev:
+        raise AttnError(f"stream: belongs to {stream.device}, the tensors are on cuda:{dev}")
+    return torch.cuda.stream(stream)
 
 
 def kv_append_q8(k_new, v_new, k_codes, v_codes, k_scales, v_scales, block_table, start_pos, device_status=None,
@@ -455,21 +470,26 @@ def kv_append_q8(k_new, v_new, k_codes, v_codes, k_scales, v_scales, block_table
     start_pos[b] + t through block_table. A block's scale is the smallest power of
     two that holds its tokens; when it grows, the block's earlier codes are
     rounded again. A NaN or an infinity makes its block read as NaN."""
-    fmt, P, page_size, Hkv, D, block = _q8_pool(k_codes, v_codes, k_scales, v_scales, block_table, start_pos,
-                                                "start_pos")
-    dev = k_codes.device
-    _need(k_new, torch.bfloat16, 4, "k_new")
-    N, T = block_table.shape[0], k_new.shape[1]
-    _q8_like(k_new, torch.bfloat16, (N, T, Hkv, D), dev, "k_new")
-    _need(v_new, torch.bfloat16, 4, "v_new")
-    _q8_like(v_new, torch.bfloat16, (N, T, Hkv, D), dev, "v_new")
-    status = _q8_status(device_status, dev)
-    with _on(dev, stream):
-        st = load_library().attn_kv_append_q8(
-            _ptr(k_new), _ptr(v_new), _ptr(k_codes), _ptr(v_codes), _ptr(k_scales), _ptr(v_scales),
-            _ptr(block_table), _ptr(start_pos), fmt, N, T, Hkv, D, page_size, block, block_table.shape[1], P,
-            status, _stream_handle(None))
-    _check(st, "attn_kv_append_q8")
+    fmt, P, page_size, Hkv, D, block, dev = _q8_pool(k_codes, v_codes, k_scales, v_scales, block_table, start_pos,
+                                                     "start_pos")
+    N, max_pages = block_table.shape
+    if not isinstance(k_new, torch.Tensor) or k_new.dim() != 4:
+        raise AttnError("k_new: expected a 4-d tensor")
+    T = k_new.shape[1]
+    _q8_buffer(k_new, _BF16, (N, T, Hkv, D), dev, "k_new")
+    _q8_buffer(v_new, _BF16, (N, T, Hkv, D), dev, "v_new")
+    status = _q8_scratch(None, 0, device_status, dev)
+    away = _q8_elsewhere(dev, stream)
+    if away is not None:
+        with away:
+            return kv_append_q8(k_new, v_new, k_codes, v_codes, k_scales, v_scales, block_table, start_pos,
+                                device_status)
+    st = load_library().attn_kv_append_q8(
+        k_new.data_ptr(), v_new.data_ptr(), k_codes.data_ptr(), v_codes.data_ptr(), k_scales.data_ptr(),
+        v_scales.data_ptr(), block_table.data_ptr(), start_pos.data_ptr(), fmt, N, T, Hkv, D, page_size, block,
+        max_pages, P, status, _raw_stream(dev))
+    if st:
+        _check(st, "attn_kv_append_q8")
 
 
 def kv_read_q8(k_codes, v_codes, k_scales, v_scales, block_table, seq_lens, k_out=None, v_out=None,
@@ -479,76 +499,81 @@ def kv_read_q8(k_codes, v_codes, k_scales, v_scales, block_table, seq_lens, k_ou
     T is that of the buffers given, else ``num_tokens``, else the block table's
     capacity. Rows at or past a sequence's length are left as they were (zero in
     buffers allocated here)."""
-    fmt, P, page_size, Hkv, D, block = _q8_pool(k_codes, v_codes, k_scales, v_scales, block_table, seq_lens,
-                                                "seq_lens")
-    dev = k_codes.device
+    fmt, P, page_size, Hkv, D, block, dev = _q8_pool(k_codes, v_codes, k_scales, v_scales, block_table, seq_lens,
+                                                     "seq_lens")
     N, max_pages = block_table.shape
-    given = k_out if k_out is not None else v_out
-    if given is not None:
-        _need(given, torch.bfloat16, 4, "k_out" if given is k_out else "v_out")
-        T = given.shape[1]
-        if num_tokens is not None and num_tokens != T:
-            raise AttnError("num_tokens differs from the buffers' rows")
-    else:
-        T = max_pages * page_size if num_tokens is None else int(num_tokens)
-    _q8_like(k_out, torch.bfloat16, (N, T, Hkv, D), dev, "k_out")
-    _q8_like(v_out, torch.bfloat16, (N, T, Hkv, D), dev, "v_out")
+    T = max_pages * page_size if num_tokens is None else int(num_tokens)
+    for name, t in (("k_out", k_out), ("v_out", v_out)):
+        if t is not None:
+            if num_tokens is None and isinstance(t, torch.Tensor) and t.dim() == 4:
+                T = num_tokens = t.shape[1]
+            _q8_buffer(t, _BF16, (N, T, Hkv, D), dev, name)
     if T < 1 or T > max_pages * page_size:
         raise AttnError("invalid number of tokens", 1)
-    status = _q8_status(device_status, dev)
-    with _on(dev, stream):
-        if k_out is None:
-            k_out = torch.zeros((N, T, Hkv, D), dtype=torch.bfloat16, device=dev)
-        if v_out is None:
-            v_out = torch.zeros((N, T, Hkv, D), dtype=torch.bfloat16, device=dev)
-        st = load_library().attn_kv_read_q8(
-            _ptr(k_codes), _ptr(v_codes), _ptr(k_scales), _ptr(v_scales), _ptr(block_table), _ptr(seq_lens),
-            _ptr(k_out), _ptr(v_out), fmt, N, T, Hkv, D, page_size, block, max_pages, P, status,
-            _stream_handle(None))
-    _check(st, "attn_kv_read_q8")
+    status = _q8_scratch(None, 0, device_status, dev)
+    away = _q8_elsewhere(dev, stream)
+    if away is not None:
+        with away:
+            return kv_read_q8(k_codes, v_codes, k_scales, v_scales, block_table, seq_lens, k_out, v_out, T,
+                              device_status)
+    if k_out is None:
+        k_out = torch.zeros((N, T, Hkv, D), dtype=_BF16, device=k_codes.device)
+    if v_out is None:
+        v_out = torch.zeros((N, T, Hkv, D), dtype=_BF16, device=k_codes.device)
+    st = load_library().attn_kv_read_q8(
+        k_codes.data_ptr(), v_codes.data_ptr(), k_scales.data_ptr(), v_scales.data_ptr(), block_table.data_ptr(),
+        seq_lens.data_ptr(), k_out.data_ptr(), v_out.data_ptr(), fmt, N, T, Hkv, D, page_size, block, max_pages, P,
+        status, _raw_stream(dev))
+    if st:
+        _check(st, "attn_kv_read_q8")
     return k_out, v_out
 
 
-def decode_q8_split_tokens(num_seqs, Hkv, max_pages, page_size) -> int:
-    """The split_tokens that decode_paged_q8 takes by itself for these sizes (0 if invalid)."""
-    return int(load_library().attn_decode_q8_split_tokens(num_seqs, Hkv, max_pages, page_size))
+def decode_paged_q8_workspace_bytes(Hq, Hkv, D) -> int:
+    """Workspace of decode_paged_q8 (0 if it refuses the sizes)."""
+    return int(load_library().attn_decode_paged_q8_workspace_bytes(Hq, Hkv, D))
 
 
-def decode_paged_q8(q, k_codes, v_codes, k_scales, v_scales, block_table, seq_lens, scale=None, split_tokens=None,
-                    out=None, lse=None, workspace=None, device_status=None, return_lse=True, stream=None):
+def decode_paged_q8(q, k_codes, v_codes, k_scales, v_scales, block_table, seq_lens, scale=None, out=None, lse=None,
+                    workspace=None, device_status=None, return_lse=True, stream=None):
     """Dense single-token decode over an 8-bit paged cache with one scale per block of tokens and head
     (uint8 E4M3 or int8 codes [P, page_size, Hkv, D], fp32 scales [P, page_size / block, Hkv]).
-    ``split_tokens`` (a multiple of 64) defaults to decode_q8_split_tokens(...); the workspace, when given,
-    must hold decode_workspace_bytes(...) for it. Returns (o [N,Hq,D] bf16, lse [N,Hq] fp32)."""
-    fmt, P, page_size, Hkv, D, block = _q8_pool(k_codes, v_codes, k_scales, v_scales, block_table, seq_lens,
-                                                "seq_lens")
-    dev = k_codes.device
-    _need(q, torch.bfloat16, 3, "q")
+    The workspace, when given, must hold decode_paged_q8_workspace_bytes(...).
+    Returns (o [N,Hq,D] bf16, lse [N,Hq] fp32)."""
+    fmt, P, page_size, Hkv, D, block, dev = _q8_pool(k_codes, v_codes, k_scales, v_scales, block_table, seq_lens,
+                                                     "seq_lens")
     N, max_pages = block_table.shape
+    if not isinstance(q, torch.Tensor) or q.dim() != 3:
+        raise AttnError("q: expected a 3-d tensor")
     Hq = q.shape[1]
-    _q8_like(q, torch.bfloat16, (N, Hq, D), dev, "q")
-    _q8_like(out, torch.bfloat16, (N, Hq, D), dev, "out")
-    _q8_like(lse, torch.float32, (N, Hq), dev, "lse")
-    scale = default_scale(D) if scale is None else scale
-    if split_tokens is None:
-        split_tokens = decode_q8_split_tokens(N, Hkv, max_pages, page_size)
-    need = decode_workspace_bytes(N, Hq, D, max_pages, page_size, split_tokens)
+    _q8_buffer(q, _BF16, (N, Hq, D), dev, "q")
+    if out is not None:
+        _q8_buffer(out, _BF16, (N, Hq, D), dev, "out")
+    if lse is not None:
+        _q8_buffer(lse, _F32, (N, Hq), dev, "lse")
+    lib = load_library()
+    need = lib.attn_decode_paged_q8_workspace_bytes(Hq, Hkv, D)
     if need == 0:
         raise AttnError("invalid decode configuration", 1)
-    if workspace is not None and (not workspace.is_contiguous() or workspace.device != dev):
-        raise AttnError(f"workspace: expected a contiguous tensor on {dev}")
-    status = _q8_status(device_status, dev)
-    with _on(dev, stream):
-        o = torch.empty_like(q) if out is None else out
-        if lse is None and return_lse:
-            lse = torch.empty((N, Hq), dtype=torch.float32, device=dev)
-        if workspace is None:
-            workspace = torch.empty(need, dtype=torch.uint8, device=dev)
-        st = load_library().attn_decode_paged_q8(
-            _ptr(q), _ptr(k_codes), _ptr(v_codes), _ptr(k_scales), _ptr(v_scales), _ptr(block_table),
-            _ptr(seq_lens), fmt, N, Hq, Hkv, D, page_size, block, max_pages, P, scale, split_tokens, _ptr(o),
-            _ptr(lse), _ptr(workspace), workspace.numel() * workspace.element_size(), status, _stream_handle(None))
-    _check(st, "attn_decode_paged_q8")
+    status = _q8_scratch(workspace, need, device_status, dev)
+    away = _q8_elsewhere(dev, stream)
+    if away is not None:
+        with away:
+            return decode_paged_q8(q, k_codes, v_codes, k_scales, v_scales, block_table, seq_lens, scale, out, lse,
+                                   workspace, device_status, return_lse)
+    o = torch.empty_like(q) if out is None else out
+    if lse is None and return_lse:
+        lse = q.new_empty((N, Hq), dtype=_F32)
+    if workspace is None:
+        workspace = q.new_empty(need, dtype=_U8)
+    st = lib.attn_decode_paged_q8(
+        q.data_ptr(), k_codes.data_ptr(), v_codes.data_ptr(), k_scales.data_ptr(), v_scales.data_ptr(),
+        block_table.data_ptr(), seq_lens.data_ptr(), fmt, N, Hq, Hkv, D, page_size, block, max_pages, P,
+        default_scale(D) if scale is None else scale, o.data_ptr(), None if lse is None else lse.data_ptr(),
+        workspace.data_ptr(), workspace.numel() * workspace.element_size(), status,
+        _raw_stream(dev))
+    if st:
+        _check(st, "attn_decode_paged_q8")
     return o, lse
 
 
@@ -562,33 +587,40 @@ def prefill_paged_q8(q, k_codes, v_codes, k_scales, v_scales, block_table, seq_l
     """Chunked prefill (as prefill_paged) over an 8-bit paged cache with block scales: q [B,Sq,Hq,D] bf16 are
     the Sq newest tokens of each sequence, already appended. The workspace, when given, must hold
     prefill_paged_q8_workspace_bytes(...). -> (o [B,Sq,Hq,D], lse [B,Hq,Sq])."""
-    fmt, P, page_size, Hkv, D, block = _q8_pool(k_codes, v_codes, k_scales, v_scales, block_table, seq_lens,
-                                                "seq_lens")
-    dev = k_codes.device
-    _need(q, torch.bfloat16, 4, "q")
+    fmt, P, page_size, Hkv, D, block, dev = _q8_pool(k_codes, v_codes, k_scales, v_scales, block_table, seq_lens,
+                                                     "seq_lens")
     B, max_pages = block_table.shape
+    if not isinstance(q, torch.Tensor) or q.dim() != 4:
+        raise AttnError("q: expected a 4-d tensor")
     Sq, Hq = q.shape[1], q.shape[2]
-    _q8_like(q, torch.bfloat16, (B, Sq, Hq, D), dev, "q")
-    _q8_like(out, torch.bfloat16, (B, Sq, Hq, D), dev, "out")
-    _q8_like(lse, torch.float32, (B, Hq, Sq), dev, "lse")
-    scale = default_scale(D) if scale is None else scale
-    need = prefill_paged_q8_workspace_bytes(B, Hkv, D, max_pages, page_size)
+    _q8_buffer(q, _BF16, (B, Sq, Hq, D), dev, "q")
+    if out is not None:
+        _q8_buffer(out, _BF16, (B, Sq, Hq, D), dev, "out")
+    if lse is not None:
+        _q8_buffer(lse, _F32, (B, Hq, Sq), dev, "lse")
+    lib = load_library()
+    need = lib.attn_prefill_paged_q8_workspace_bytes(B, Hkv, D, max_pages, page_size)
     if need == 0:
         raise AttnError("invalid prefill configuration", 1)
-    if workspace is not None and (not workspace.is_contiguous() or workspace.device != dev):
-        raise AttnError(f"workspace: expected a contiguous tensor on {dev}")
-    status = _q8_status(device_status, dev)
-    with _on(dev, stream):
-        o = torch.empty_like(q) if out is None else out
-        if lse is None and return_lse:
-            lse = torch.empty((B, Hq, Sq), dtype=torch.float32, device=dev)
-        if workspace is None:
-            workspace = torch.empty(need, dtype=torch.uint8, device=dev)
-        st = load_library().attn_prefill_paged_q8(
-            _ptr(q), _ptr(k_codes), _ptr(v_codes), _ptr(k_scales), _ptr(v_scales), _ptr(block_table),
-            _ptr(seq_lens), _ptr(o), _ptr(lse), fmt, B, Sq, Hq, Hkv, D, page_size, block, max_pages, P, scale,
-            _ptr(workspace), workspace.numel() * workspace.element_size(), status, _stream_handle(None))
-    _check(st, "attn_prefill_paged_q8")
+    status = _q8_scratch(workspace, need, device_status, dev)
+    away = _q8_elsewhere(dev, stream)
+    if away is not None:
+        with away:
+            return prefill_paged_q8(q, k_codes, v_codes, k_scales, v_scales, block_table, seq_lens, scale, out, lse,
+                                    workspace, device_status, return_lse)
+    o = torch.empty_like(q) if out is None else out
+    if lse is None and return_lse:
+        lse = q.new_empty((B, Hq, Sq), dtype=_F32)
+    if workspace is None:
+        workspace = q.new_empty(need, dtype=_U8)
+    st = lib.attn_prefill_paged_q8(
+        q.data_ptr(), k_codes.data_ptr(), v_codes.data_ptr(), k_scales.data_ptr(), v_scales.data_ptr(),
+        block_table.data_ptr(), seq_lens.data_ptr(), o.data_ptr(), None if lse is None else lse.data_ptr(), fmt, B,
+        Sq, Hq, Hkv, D, page_size, block, max_pages, P, default_scale(D) if scale is None else scale,
+        workspace.data_ptr(), workspace.numel() * workspace.element_size(), status,
+        _raw_stream(dev))
+    if st:
+        _check(st, "attn_prefill_paged_q8")
     return o, lse
 
 

@@ -99,6 +99,21 @@ int encode_map5(CUtensorMap* map, const void* base, const uint64_t dims[5], cons
   return r == CUDA_SUCCESS ? ATTN_OK : ATTN_ERR_INVALID_ARG;
 }
 
+// 3-D map of bytes with the 128-byte swizzle. dims/box innermost first; strides in bytes for dims 1, 2.
+int encode_map3_u8(CUtensorMap* map, const void* base, const uint64_t dims[3], const uint64_t strides[2],
+                   const uint32_t box[3]) {
+  auto enc = tensor_map_encoder();
+  if (!enc) return ATTN_ERR_CUDA;
+  const cuuint32_t elem_strides[3] = {1, 1, 1};
+  cuuint64_t d[3] = {dims[0], dims[1], dims[2]};
+  cuuint64_t s[2] = {strides[0], strides[1]};
+  cuuint32_t b[3] = {box[0], box[1], box[2]};
+  const CUresult r = enc(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, const_cast<void*>(base), d, s, b, elem_strides,
+                         CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_128B,
+                         CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  return r == CUDA_SUCCESS ? ATTN_OK : ATTN_ERR_INVALID_ARG;
+}
+
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
 // Once per device and kernel (one mask per kernel, keyed by the kernel itself): check that it
@@ -559,32 +574,72 @@ bool valid_q8_block(int block, int page_size) {
   return valid_page_size(page_size) && valid_page_size(block) && block <= page_size;
 }
 
-template <int D, int GP, bool I8>
-int launch_decode_q8(const CUtensorMap& tk, const CUtensorMap& tv, const DecodeQ8Params& qp, int* ticket_counter,
-                     int sms, cudaStream_t stream) {
-  using L = DecodeQ8Smem<D, GP, I8>;
-  if (int st = set_smem_once<decode_q8_kernel<D, GP, I8>>(L::kDynamic)) return st;
-  const long long items = (long long)qp.d.max_splits * qp.d.num_seqs * qp.d.Hkv;
-  const long long slots = (long long)sms * L::kBlocks;
-  DecodeQ8Params pk = qp;
-  pk.d.static_items = items <= slots ? 1 : 0;   // one item per CTA: no ticket counter to zero
-  if (!pk.d.static_items && cudaMemsetAsync(ticket_counter, 0, sizeof(int), stream) != cudaSuccess)
-    return ATTN_ERR_CUDA;
-  decode_q8_kernel<D, GP, I8><<<dim3(unsigned(items < slots ? items : slots)), dim3(kQ8Threads), L::kDynamic,
-                                stream>>>(tk, tv, pk, ticket_counter);
+template <int D, int NH, int GP, bool I8>
+int launch_decode_q8(const CUtensorMap& tk, const CUtensorMap& tv, DecodeQ8Params& p, int sms, cudaStream_t stream) {
+  using L = DecodeQ8Smem<D, NH, GP, I8>;
+  if (int st = set_smem_once<decode_q8_kernel<D, NH, GP, I8>>(L::kDynamic)) return st;
+  const int ctas = sms * L::kBlocks < kQ8MaxCtas ? sms * L::kBlocks : kQ8MaxCtas;
+  p.teams = ctas / p.team;
+  const unsigned grid = unsigned(p.teams * p.team);
+  decode_q8_kernel<D, NH, GP, I8><<<dim3(grid), dim3(kQ8Threads), L::kDynamic, stream>>>(tk, tv, p);
   if (int st = launch_status()) return st;
-  return launch_merge<D>(qp.d, stream);
+  cudaLaunchAttribute attr[1];   // scheduled while the last CTAs run; waits for them before it reads
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(grid, unsigned(p.part_rows));
+  cfg.blockDim = dim3(D);
+  cfg.stream = stream;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  if (cudaLaunchKernelEx(&cfg, decode_q8_merge_kernel<D>, p) != cudaSuccess) return ATTN_ERR_CUDA;
+  return launch_status();
 }
 
-// The digits of up to GP query heads are the columns of the products: the next power of two of G.
-template <int D, bool I8>
-int dispatch_decode_q8(const CUtensorMap& tk, const CUtensorMap& tv, const DecodeQ8Params& qp, int* ticket_counter,
-                       int sms, cudaStream_t s) {
-  if (qp.G == 1) return launch_decode_q8<D, 1, I8>(tk, tv, qp, ticket_counter, sms, s);
-  if (qp.G == 2) return launch_decode_q8<D, 2, I8>(tk, tv, qp, ticket_counter, sms, s);
-  if (qp.G <= 4) return launch_decode_q8<D, 4, I8>(tk, tv, qp, ticket_counter, sms, s);
-  if (qp.G <= 8) return launch_decode_q8<D, 8, I8>(tk, tv, qp, ticket_counter, sms, s);
-  return launch_decode_q8<D, 16, I8>(tk, tv, qp, ticket_counter, sms, s);
+// The digits of up to GP query heads of each KV head are the columns of the products: the next power of two of G.
+template <bool I8>
+int dispatch_decode_q8(int D, const CUtensorMap& tk, const CUtensorMap& tv, DecodeQ8Params& p, int sms,
+                       cudaStream_t s) {
+  if (D == 128) {
+    if (p.G == 1) return launch_decode_q8<128, 1, 1, I8>(tk, tv, p, sms, s);
+    if (p.G == 2) return launch_decode_q8<128, 1, 2, I8>(tk, tv, p, sms, s);
+    if (p.G <= 4) return launch_decode_q8<128, 1, 4, I8>(tk, tv, p, sms, s);
+    if (p.G <= 8) return launch_decode_q8<128, 1, 8, I8>(tk, tv, p, sms, s);
+    return launch_decode_q8<128, 1, 16, I8>(tk, tv, p, sms, s);
+  }
+  if (p.solo) return launch_decode_q8<64, 1, 16, I8>(tk, tv, p, sms, s);
+  if (p.G == 1) return launch_decode_q8<64, 2, 1, I8>(tk, tv, p, sms, s);
+  if (p.G == 2) return launch_decode_q8<64, 2, 2, I8>(tk, tv, p, sms, s);
+  if (p.G <= 4) return launch_decode_q8<64, 2, 4, I8>(tk, tv, p, sms, s);
+  return launch_decode_q8<64, 2, 8, I8>(tk, tv, p, sms, s);
+}
+
+// Lanes of a team: at most 8 of the 128-byte rows of a token, with the fewest idle lanes in the last group.
+int q8_team(int rows) {
+  int best = 1, idle = 0;
+  for (int t = 2; t <= kQ8MaxTeam && t <= rows; ++t) {
+    const int waste = (rows + t - 1) / t * t - rows;
+    // a wider team is worth a few per cent of idle lanes: it keeps neighbouring rows together
+    if (waste * 16 <= rows || waste <= idle) { best = t; idle = waste; }
+  }
+  return best;
+}
+
+// Workspace of the decode over an 8-bit cache: {cut sequence} per CTA, log2-sum-exps, parts of O.
+struct DecodeQ8Layout {
+  size_t lse_off = 0, o_off = 0, total = 0;
+  int part_rows = 0;
+};
+bool decode_q8_layout(int Hq, int Hkv, int D, DecodeQ8Layout* L) {
+  if (Hq < 1 || Hkv < 1 || Hq % Hkv != 0 || (D != 64 && D != 128)) return false;
+  const int G = Hq / Hkv;
+  if (G > 16) return false;
+  L->part_rows = D == 64 && G <= 8 ? 2 * G : G;
+  const size_t rows = size_t(kQ8MaxCtas) * 2 * size_t(L->part_rows);
+  L->lse_off = (size_t(kQ8MaxCtas) * sizeof(int4) + 255) / 256 * 256;
+  L->o_off = (L->lse_off + rows * sizeof(float) + 255) / 256 * 256;
+  L->total = L->o_off + rows * size_t(D) * sizeof(float);
+  return true;
 }
 
 template <int D, bool I8>
@@ -1091,81 +1146,67 @@ int attn_kv_read_q8(const void* k_codes, const void* v_codes, const float* k_sca
   return launch_read_q8(format, D, p, sms, static_cast<cudaStream_t>(stream));
 }
 
-int attn_decode_q8_split_tokens(int num_seqs, int Hkv, int max_pages_per_seq, int page_size) {
-  if (num_seqs < 1 || Hkv < 1 || max_pages_per_seq < 1 || !valid_page_size(page_size)) return 0;
-  const long long cap = (long long)max_pages_per_seq * page_size;
-  if (cap > (1ll << 30)) return 0;
-  // two CTAs on each of the 148 SMs: one item for each while that leaves at most 1024 tokens to an item,
-  // items of 1024 tokens beyond
-  const long long per = (long long)num_seqs * Hkv * ((cap + kQ8Tok - 1) / kQ8Tok);   // tiles, at most
-  long long split = (per + 295) / 296 * kQ8Tok;
-  if (split > 1024) split = 1024;
-  return int(split);
+size_t attn_decode_paged_q8_workspace_bytes(int Hq, int Hkv, int D) {
+  DecodeQ8Layout L;
+  return decode_q8_layout(Hq, Hkv, D, &L) ? L.total : 0;
 }
 
 int attn_decode_paged_q8(const void* q, const void* k_codes, const void* v_codes, const float* k_scales,
                          const float* v_scales, const int32_t* block_table, const int32_t* seq_lens, int format,
                          int num_seqs, int Hq, int Hkv, int D, int page_size, int scale_block, int max_pages_per_seq,
-                         int num_pages, float scale, int split_tokens, void* o, float* lse, void* workspace,
-                         size_t workspace_bytes, int* device_status, void* stream) {
+                         int num_pages, float scale, void* o, float* lse, void* workspace, size_t workspace_bytes,
+                         int* device_status, void* stream) {
   if (!q || !o || !workspace || !aligned16(q) || !aligned16(o) || !aligned16(workspace) || !aligned4(lse))
     return ATTN_ERR_INVALID_ARG;
   if (int st = check_q8_pool(k_codes, v_codes, k_scales, v_scales, block_table, seq_lens, format, num_seqs, Hkv, D,
                              page_size, scale_block, max_pages_per_seq, num_pages))
     return st;
   if (Hq < 1 || Hq % Hkv != 0) return ATTN_ERR_INVALID_ARG;
-  // merge CTAs: one per (sequence, head), or one per 32 of its head dimensions
-  if ((long long)num_seqs * Hq * (D / 32) > 0x7fffffffll) return ATTN_ERR_INVALID_ARG;
-  if (split_tokens < 64 || split_tokens % 64 != 0) return ATTN_ERR_INVALID_ARG;
   if (!std::isfinite(scale) || !(scale > 0.f)) return ATTN_ERR_INVALID_ARG;
   const int G = Hq / Hkv;
   if (G > 16) return ATTN_ERR_UNSUPPORTED;
-  const size_t need = attn_decode_workspace_bytes(num_seqs, Hq, D, max_pages_per_seq, page_size, split_tokens);
-  if (need == 0 || workspace_bytes < need) return ATTN_ERR_INVALID_ARG;
+  DecodeQ8Layout L;
+  if (!decode_q8_layout(Hq, Hkv, D, &L) || workspace_bytes < L.total) return ATTN_ERR_INVALID_ARG;
   int sms = 0;
   if (int st = current_device(&sms)) return st;
 
-  DecodeQ8Params qp{};
-  DecodeParams& p = qp.d;
+  DecodeQ8Params p{};
   p.q = static_cast<const __nv_bfloat16*>(q);
   p.block_table = block_table;
   p.seq_lens = seq_lens;
+  p.k_scales = k_scales;
+  p.v_scales = v_scales;
   p.o = static_cast<__nv_bfloat16*>(o);
   p.lse = lse;
-  const long long ms = max_splits_of(max_pages_per_seq, page_size, split_tokens);
-  int* ticket_counter = static_cast<int*>(workspace);
-  p.ws_o = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + kWsHeader);
-  size_t o_bytes = 0;
-  decode_ws_bytes(size_t(num_seqs) * size_t(ms), size_t(Hq), size_t(D), &o_bytes);   // checked above
-  p.ws_lse = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + kWsHeader + (o_bytes + 255) / 256 * 256);
+  uint8_t* ws = static_cast<uint8_t*>(workspace);
+  p.ws_cut = reinterpret_cast<int4*>(ws);
+  p.ws_lse = reinterpret_cast<float*>(ws + L.lse_off);
+  p.ws_o = reinterpret_cast<float*>(ws + L.o_off);
   p.status = device_status;
-  p.num_seqs = num_seqs; p.Hq = Hq; p.Hkv = Hkv;
-  p.page_size = page_size; p.max_pages = max_pages_per_seq; p.num_pages = num_pages;
-  p.split_tokens = split_tokens;
-  p.max_splits = int(ms);
+  p.num_seqs = num_seqs; p.Hq = Hq; p.Hkv = Hkv; p.G = G;
+  p.max_pages = max_pages_per_seq; p.num_pages = num_pages; p.page_size = page_size;
+  p.page_shift = log2_of(page_size);
+  p.block_shift = log2_of(scale_block);
+  p.box = page_size < kQ8MaxBox ? page_size : kQ8MaxBox;
+  p.solo = D == 64 && G > 8 ? 1 : 0;
+  p.rows128 = D == 128 || p.solo ? Hkv : (Hkv + 1) / 2;
+  p.team = q8_team(p.rows128);
+  p.groups = (p.rows128 + p.team - 1) / p.team;
+  p.part_rows = L.part_rows;
   p.scale_log2 = scale * 1.4426950408889634f;
-  p.log2_lambda = -INFINITY;
-  qp.k_scales = k_scales;
-  qp.v_scales = v_scales;
-  qp.G = G;
-  qp.page_shift = log2_of(page_size);
-  qp.block_shift = log2_of(scale_block);
 
-  // code pool [P][page_size][Hkv][D] as a 4-D map {D, page_size, Hkv, P}; box = 16 slots of one head,
-  // landing as 16 rows of D bytes under the swizzle of that width
-  const uint64_t dims[4] = {uint64_t(D), uint64_t(page_size), uint64_t(Hkv), uint64_t(num_pages)};
-  const uint64_t strides[3] = {uint64_t(Hkv) * D, uint64_t(D), uint64_t(page_size) * Hkv * D};
-  const uint32_t box[4] = {uint32_t(D), uint32_t(kQ8Chunk), 1, 1};
-  const CUtensorMapSwizzle swizzle = D == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B;
+  // code pool as a 3-D map {Hkv * D bytes of a token, page_size, P}; box = 16 to 64 slots of 128 bytes, landing
+  // as 128-byte rows under the 128-byte swizzle; bytes past the last head read as zeros
+  const uint64_t token = uint64_t(Hkv) * D;
+  const uint64_t dims[3] = {token, uint64_t(page_size), uint64_t(num_pages)};
+  const uint64_t strides[2] = {token, token * page_size};
+  const uint32_t box[3] = {uint32_t(kQ8Row), uint32_t(p.box), 1};
   CUtensorMap tk, tv;
-  if (int st = encode_map(&tk, k_codes, dims, strides, box, swizzle, CU_TENSOR_MAP_DATA_TYPE_UINT8)) return st;
-  if (int st = encode_map(&tv, v_codes, dims, strides, box, swizzle, CU_TENSOR_MAP_DATA_TYPE_UINT8)) return st;
+  if (int st = encode_map3_u8(&tk, k_codes, dims, strides, box)) return st;
+  if (int st = encode_map3_u8(&tv, v_codes, dims, strides, box)) return st;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  if (format == ATTN_KV_INT8)
-    return D == 128 ? dispatch_decode_q8<128, true>(tk, tv, qp, ticket_counter, sms, s)
-                    : dispatch_decode_q8<64, true>(tk, tv, qp, ticket_counter, sms, s);
-  return D == 128 ? dispatch_decode_q8<128, false>(tk, tv, qp, ticket_counter, sms, s)
-                  : dispatch_decode_q8<64, false>(tk, tv, qp, ticket_counter, sms, s);
+  return format == ATTN_KV_INT8 ? dispatch_decode_q8<true>(D, tk, tv, p, sms, s)
+                                : dispatch_decode_q8<false>(D, tk, tv, p, sms, s);
 }
 
 size_t attn_prefill_paged_q8_workspace_bytes(int num_seqs, int Hkv, int D, int max_pages_per_seq, int page_size) {

@@ -9,7 +9,7 @@
 // split into two 8-bit digits so that nothing of it is lost:
 //   S^T = Kc (128 tokens x D) * [q_hi; q_lo]^T,  q * 2^a = q_hi + q_lo / 16 (E4M3)
 //                                                        = 256 q_hi + q_lo  (int8)
-//   O^T_w = Vc^T (D x 32 tokens) * [p_hi; p_lo]^T        for each warp w's 32 tokens
+//   O^T_w = Vc^T (128 dims x 32 tokens) * [p_hi; p_lo]^T  for each warp w's 32 tokens
 // E4M3: a bf16 value has 8 significant bits, a code 4, so two codes hold q exactly
 // down to 2^-14 of the row's largest value; the products accumulate in fp32.
 // int8: q becomes a 16-bit integer (exact down to 2^-8 of the row's largest value)
@@ -18,14 +18,36 @@
 // the value scale is part of the exponent, so p <= 1 whatever the scales are. Two
 // E4M3 digits keep 8 significant bits of 256 p, two int8 digits keep p to 2^-16.
 //
-// A CTA has four softmax warps (one token per thread of a 128-token tile), a
-// producer warp (TMA copies of 16 slots, scales by cp.async) and an MMA warp.
+// A tile is 128 tokens x 128 bytes of K and of V: one KV head of D = 128, or two
+// neighbouring heads of D = 64 (NH = 2), whose scores come from the two halves of
+// the row into columns of their own and whose O^T are the two halves of the lanes.
+// So a copy always moves 128-byte rows, and one shape of every product serves both.
+// (D = 64 with more than 8 query heads a group takes one head of the row at a time
+// and reads the row twice: the digits of both would not fit the tensor memory.)
+//
+// Work. The batch's tiles in the order (head group, sequence, tile) are cut into as
+// many equal runs as there are teams; a team is one CTA for each of up to 8
+// neighbouring rows of 128 bytes ("lanes"), which walk the same run. Neighbouring
+// 128-byte rows are thus read at about the same time: with each CTA on its own work
+// the same copies reach 5.0 to 5.5 TB/s instead of 6.5. A sequence that lies inside a
+// run is written at once; the parts of one that is cut are merged by
+// decode_q8_merge_kernel, and each CTA has two at most, whatever the lengths.
+//
+// A CTA has four softmax warps (one token per thread of a tile), two producer warps
+// (one walks the lengths and block tables, copies K by TMA and the scales by
+// cp.async, and hands each tile's pages to the other, which copies V: one warp
+// takes about 100 cycles to issue a copy, and 16-token pages need 16 of them a
+// tile, so with one producer the issue took longer than the tile's share of the
+// HBM time, 2570 cycles with two CTAs per SM), a warp that turns the query rows
+// into digits and issues the score products, and one that issues the P V products.
+// Scores run a tile ahead of the softmax, and O of a tile is added to the
+// accumulators while the next tile's P V runs (S^T, P and O^T are double-buffered).
 // Each softmax warp keeps its own running maxima X, Y for its 32 tokens of every
 // tile, and its own accumulator columns, so the warps exchange no maximum: the
 // P V product of a tile is four MMAs of K = 32, one per warp. O stays in fp32
 // registers (thread = head dimension) and is rescaled there by each warp's
 // factor, which is why TMEM holds only the tile's own products. The four
-// accumulators are merged when the item (sequence, split, KV head) ends.
+// accumulators are merged when the CTA's part of the sequence ends.
 #pragma once
 
 #include "decode.cuh"
@@ -33,60 +55,86 @@
 namespace attn {
 
 constexpr int kQ8Tok = 128;          // tokens per tile
-constexpr int kQ8Chunk = 16;         // tokens per TMA copy (a block-table page is a multiple of it)
+constexpr int kQ8Row = 128;          // bytes of a tile's row
+constexpr int kQ8Chunk = 16;         // tokens whose page and scales are looked up together
+constexpr int kQ8MaxBox = 64;        // tokens per TMA copy: min(page_size, 64)
 constexpr int kQ8SoftmaxWarps = 4;
-constexpr int kQ8Threads = (kQ8SoftmaxWarps + 2) * 32;
+constexpr int kQ8KWarp = kQ8SoftmaxWarps, kQ8VWarp = kQ8KWarp + 1, kQ8ScoreWarp = kQ8KWarp + 2,
+              kQ8PvWarp = kQ8KWarp + 3;
+constexpr int kQ8Threads = (kQ8SoftmaxWarps + 4) * 32;
+constexpr int kQ8Scan = 64;          // sums of tile counts, one for each four threads' sequences
+constexpr int kQ8MaxTeam = 8;        // lanes of a team
+constexpr int kQ8MaxCtas = 320;      // CTAs of a call at most (two on each of 148 SMs); fixes the workspace size
 
 struct DecodeQ8Params {
-  DecodeParams d;         // shared with the merge; scale_log2 does not contain the K scale
-  const float* k_scales;  // [num_pages][page_size / block][Hkv]
+  const __nv_bfloat16* q;      // [N][Hq][D]
+  const int32_t* block_table;  // [N][max_pages]
+  const int32_t* seq_lens;     // [N]
+  const float* k_scales;       // [num_pages][page_size / block][Hkv]
   const float* v_scales;
-  int G;                  // query heads per KV head (<= GP)
-  int page_shift;         // log2(page_size)
-  int block_shift;        // log2(tokens per scale)
+  __nv_bfloat16* o;            // [N][Hq][D]
+  float* lse;                  // [N][Hq] (natural log) or null
+  float* ws_o;                 // [CTA][2][rows][D] fp32 parts of cut sequences (normalised)
+  float* ws_lse;               // [CTA][2][rows] their log2-sum-exp
+  int4* ws_cut;                // [CTA] the cut sequence whose first part this CTA holds: {seq, group, last team, slot}
+  int* status;                 // caller's device status word or null
+  int num_seqs, Hq, Hkv, G, max_pages, num_pages, page_size;
+  int page_shift;              // log2(page_size)
+  int block_shift;             // log2(tokens per scale)
+  int box;                     // tokens per TMA copy
+  int rows128;                 // 128-byte rows of a token that items are made of (solo: one per KV head)
+  int solo;                    // D = 64, one head of a row at a time
+  int team, groups, teams;     // lanes of a team, ceil(rows128 / team), teams
+  int part_rows;               // query rows of a part: G, or 2 G for two heads
+  float scale_log2;            // softmax scale * log2(e), without the K scale
 };
 
-template <int D, int GP, bool I8>
+template <int D, int NH, int GP, bool I8>
 struct DecodeQ8Smem {
-  static constexpr int kN = GP <= 8 ? 16 : 32;             // columns of S^T and of each O^T_w: hi digits, lo digits
-  static constexpr int kTileBytes = kQ8Tok * D;            // K (or V) codes of one tile
-  static constexpr int kQBytes = GP * D * 2;               // the item's query rows
-  static constexpr int kStageBytes = (2 * kTileBytes + kQBytes + 1023) / 1024 * 1024;
-  static constexpr int kBlocks = GP <= 8 ? 2 : 1;          // resident CTAs per SM
-  static constexpr int kQTile = kN * D;                    // digit rows of q
+  static constexpr int kR = NH * GP;                       // digit rows: head half * GP + query head
+  static constexpr int kN = kR <= 8 ? 16 : 32;             // columns of a product: hi digits, lo digits
+  static constexpr int kTileBytes = kQ8Tok * kQ8Row;       // K (or V) codes of one tile
+  static constexpr int kStageBytes = 2 * kTileBytes;
+  static constexpr int kQBytes = kR * D * 2;               // the query rows of an item
+  static constexpr int kBlocks = kR <= 8 ? 2 : 1;          // resident CTAs per SM
+  static constexpr int kQTile = kN * kQ8Row;               // digit rows of q
   static constexpr int kPTile = kN * kQ8Tok;               // digit rows of P
-  static constexpr int kSmall = 64 + 32 + 4 * (2 * 4 * GP + 3 * 4 * GP + GP) + 16 * 8;   // per stage extras below
-  static constexpr int kFit =
-      (233472 / kBlocks - 1024 - 1024 - kQTile - kPTile - kSmall - 256) / (kStageBytes + 64 + 32 + 16);
+  static constexpr int kPerStage = kStageBytes + kQBytes + 64 * NH + 32 + 48 + 24;
+  static constexpr int kFixed = 1024 + 2 * kQTile + 2 * kPTile + 4 * (4 * 4 * kR + 3 * 4 * kR + 2 * kR) + 4 * kQ8Scan +
+                                8 * 13 + 64;
+  static constexpr int kFit = (233472 / kBlocks - 1024 - kFixed) / kPerStage;
   static constexpr int kStages = kFit < 8 ? kFit : 8;
-  static constexpr int kQT = kStages * kStageBytes;                    // q digits (1024-byte aligned)
-  static constexpr int kPT = kQT + (kQTile + 1023) / 1024 * 1024;      // P digits
-  static constexpr int kScales = kPT + kPTile;                         // [stage][K 8 | V 8] floats
-  static constexpr int kInfo = kScales + 64 * kStages;                 // TileInfo per stage
-  static constexpr int kAlpha = kInfo + 32 * kStages;                  // [2][warp][GP] floats
-  static constexpr int kMl = kAlpha + 4 * 2 * 4 * GP;                  // [warp][GP] x {X, Y, l} floats
-  static constexpr int kQf = kMl + 4 * 3 * 4 * GP;                     // [GP] floats
-  static constexpr int kBars = (kQf + 4 * GP + 7) / 8 * 8;             // mbarriers
-  // full[kStages], empty[kStages], s_full[2], p_ready, o_full, q_ready, ml_ready, done
-  static constexpr int kTotal = kBars + 8 * (2 * kStages + 7);
+  static constexpr int kQT = kStages * kStageBytes;                    // q digits [item parity], 1024-byte aligned
+  static constexpr int kPT = kQT + 2 * kQTile;                         // P digits [tile parity]
+  static constexpr int kQRows = kPT + 2 * kPTile;                      // query rows per stage
+  static constexpr int kScales = kQRows + kQBytes * kStages;           // [stage][head half][K 8 | V 8] floats
+  static constexpr int kInfo = kScales + 64 * NH * kStages;               // TileInfo per stage
+  static constexpr int kJob = kInfo + 32 * kStages;                    // V copies of a stage: 8 pages, t0, byte, mask
+  static constexpr int kAlpha = kJob + 48 * kStages;                   // [tile mod 4][warp][kR] floats
+  static constexpr int kMl = kAlpha + 4 * 4 * 4 * kR;                  // [warp][kR] x {X, Y, l} floats
+  static constexpr int kQf = kMl + 4 * 3 * 4 * kR;                     // [item parity][kR] floats
+  static constexpr int kScan = (kQf + 4 * 2 * kR + 7) / 8 * 8;         // sums of tile counts
+  static constexpr int kBars = (kScan + 4 * kQ8Scan + 7) / 8 * 8;      // mbarriers
+  // full[kStages], empty[kStages], v_go[kStages], s_full[2], s_free[2], p_ready[2], o_full[2], q_ready[2],
+  // ml_ready, done[2]
+  static constexpr int kTotal = kBars + 8 * (3 * kStages + 13);
   static constexpr int kDynamic = kTotal + 1024;
-  static constexpr int kTmemUse = 2 * kN + 4 * kN;
-  static constexpr int kTmemCols = kTmemUse <= 128 ? 128 : 256;
+  static constexpr int kSBuf = NH * kN;                    // columns of one score buffer: kN for each head half
+  static constexpr int kTmemUse = 2 * kSBuf + 2 * 4 * kN;
+  static constexpr int kTmemCols = kTmemUse <= 256 ? 256 : 512;
   static_assert(kDynamic <= 233472 / kBlocks - 1024, "shared memory per block");
-  static_assert(kStages >= 2, "ring depth");
+  static_assert(kStages >= 3, "ring depth");
+  static_assert(kQ8Scan * 4 == kQ8Threads, "four threads a sum");
   static_assert(kTmemUse <= kTmemCols && kTmemCols * kBlocks <= 512, "tensor memory");
+  static_assert(kR <= 16, "digit rows");
 };
 
-__device__ __forceinline__ bool mbar_test_wait(uint64_t* bar, uint32_t parity) {
-  uint32_t ok;
+__device__ __forceinline__ void tma_load_3d(void* dst, const CUtensorMap* map, uint64_t* bar, int c0, int c1, int c2) {
   asm volatile(
-      "{\n\t.reg .pred p;\n\t"
-      "mbarrier.test_wait.parity.acquire.cta.shared::cta.b64 p, [%1], %2;\n\t"
-      "selp.u32 %0, 1, 0, p;\n\t}"
-      : "=r"(ok)
-      : "r"(smem_u32(bar)), "r"(parity)
+      "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%3, %4, %5}], [%2];" ::"r"(smem_u32(dst)),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(smem_u32(bar)), "r"(c0), "r"(c1), "r"(c2)
       : "memory");
-  return ok != 0;
 }
 // 4-byte asynchronous copies, and their arrival on an mbarrier once they have landed.
 __device__ __forceinline__ void cp_async4(void* dst, const void* src) {
@@ -122,30 +170,19 @@ __host__ __device__ constexpr uint32_t make_idesc_q8(int M, int N, int a_mn_majo
   return (uint32_t(I8 ? 2 : 1) << 4) | (uint32_t(I8 ? 1 : 0) << 7) | (uint32_t(I8 ? 1 : 0) << 10) |
          (uint32_t(a_mn_major) << 15) | (uint32_t(N >> 3) << 17) | (uint32_t(M >> 4) << 24);
 }
-// Shared-memory descriptor of a tile of 128-byte or 64-byte rows under the swizzle of that width;
-// eight-row atoms follow one another, so the stride between them is eight rows.
-template <int ROW>
-__device__ __forceinline__ uint64_t make_sdesc_rows(uint32_t smem_addr) {
-  static_assert(ROW == 128 || ROW == 64, "swizzled rows");
-  uint64_t d = 0;
-  d |= uint64_t((smem_addr >> 4) & 0x3FFFu);
-  d |= uint64_t(1) << 16;                          // leading offset: not used, one atom covers it
-  d |= uint64_t((8 * ROW) >> 4) << 32;
-  d |= uint64_t(1) << 46;                          // descriptor version for sm_100
-  d |= uint64_t(ROW == 128 ? 2 : 4) << 61;         // 128-byte or 64-byte swizzle
-  return d;
-}
+// Shared-memory descriptor of a tile of 128-byte rows under the 128-byte swizzle, its eight-row
+// atoms 1024 bytes apart (both for K-major and for MN-major operands of 128 bytes).
+__device__ __forceinline__ uint64_t make_sdesc_rows(uint32_t smem_addr) { return make_sdesc_sw128(smem_addr, 16, 1024); }
 // Byte offset of 16-byte unit c of row r in such a tile.
-template <int ROW>
-__device__ __forceinline__ uint32_t row_unit(int r, int c) {
-  return ROW == 128 ? uint32_t(r * 128 + ((c ^ (r & 7)) << 4)) : uint32_t(r * 64 + ((c ^ ((r >> 1) & 3)) << 4));
-}
+__device__ __forceinline__ uint32_t row_unit(int r, int c) { return uint32_t(r * 128 + ((c ^ (r & 7)) << 4)); }
 
 // NC columns of 32-bit TMEM of this warp's 32 lanes -> registers; no wait (tmem_ld_wait, then reg_fence).
 template <int NC>
 __device__ __forceinline__ void tmem_ld_cols(uint32_t taddr, uint32_t* r) {
-  static_assert(NC == 2 || NC == 4 || NC == 8 || NC == 16 || NC == 32, "columns");
-  if constexpr (NC == 2) {
+  static_assert(NC == 1 || NC == 2 || NC == 4 || NC == 8 || NC == 16 || NC == 32, "columns");
+  if constexpr (NC == 1) {
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x1.b32 {%0}, [%1];" : "=r"(r[0]) : "r"(taddr) : "memory");
+  } else if constexpr (NC == 2) {
     asm volatile("tcgen05.ld.sync.aligned.32x32b.x2.b32 {%0,%1}, [%2];" : "=r"(r[0]), "=r"(r[1]) : "r"(taddr) : "memory");
   } else if constexpr (NC == 4) {
     asm volatile("tcgen05.ld.sync.aligned.32x32b.x4.b32 {%0,%1,%2,%3}, [%4];"
@@ -218,28 +255,36 @@ __device__ __forceinline__ float join_digits(uint32_t hi, uint32_t lo) {
   else return fmaf(__uint_as_float(lo), 0.0625f, __uint_as_float(hi));
 }
 
-template <int D, int GP, bool I8>
-__global__ void __launch_bounds__(kQ8Threads, DecodeQ8Smem<D, GP, I8>::kBlocks)
+// Tiles of a sequence of (clamped) length `len`.
+__device__ __forceinline__ int q8_tiles(int len) { return (len + kQ8Tok - 1) / kQ8Tok; }
+__device__ __forceinline__ int q8_clamp_len(int len, int capacity) { return len < 0 ? 0 : min(len, capacity); }
+
+template <int D, int NH, int GP, bool I8>
+__global__ void __launch_bounds__(kQ8Threads, DecodeQ8Smem<D, NH, GP, I8>::kBlocks)
     decode_q8_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
-                     const DecodeQ8Params qp, int* ticket_counter) {
-  using L = DecodeQ8Smem<D, GP, I8>;
+                     const DecodeQ8Params p) {
+  static_assert(D == 64 || (D == 128 && NH == 1), "heads of a 128-byte row");
+  using L = DecodeQ8Smem<D, NH, GP, I8>;
   launch_dependents();   // the merge is scheduled early; it waits for this grid to finish
   constexpr int NS = L::kStages;
   constexpr int KN = L::kN;
-  const DecodeParams& p = qp.d;
+  constexpr int R = L::kR;
 
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   float* scales = reinterpret_cast<float*>(smem + L::kScales);
   TileInfo* info = reinterpret_cast<TileInfo*>(smem + L::kInfo);
+  int* scan = reinterpret_cast<int*>(smem + L::kScan);
   uint64_t* full = reinterpret_cast<uint64_t*>(smem + L::kBars);
   uint64_t* empty = full + NS;
-  uint64_t* s_full = empty + NS;     // [2]
-  uint64_t* p_ready = s_full + 2;
-  uint64_t* o_full = p_ready + 1;
-  uint64_t* q_ready = o_full + 1;
-  uint64_t* ml_ready = q_ready + 1;
-  uint64_t* done = ml_ready + 1;
+  uint64_t* v_go = empty + NS;       // a stage's V copies may be issued
+  uint64_t* s_full = v_go + NS;      // [2]
+  uint64_t* s_free = s_full + 2;     // [2]
+  uint64_t* p_ready = s_free + 2;    // [2]
+  uint64_t* o_full = p_ready + 2;    // [2]
+  uint64_t* q_ready = o_full + 2;    // [2]
+  uint64_t* ml_ready = q_ready + 2;
+  uint64_t* done = ml_ready + 1;     // [2]
   __shared__ int abort_word;
   __shared__ uint32_t tmem_slot;
   volatile int* abort_flag = &abort_word;
@@ -247,30 +292,48 @@ __global__ void __launch_bounds__(kQ8Threads, DecodeQ8Smem<D, GP, I8>::kBlocks)
   const int warp = threadIdx.x >> 5;
   const int lane = threadIdx.x & 31;
   const int capacity = p.max_pages * p.page_size;
-  const long long num_items = (long long)p.max_splits * p.num_seqs * p.Hkv;
 
   if (threadIdx.x == 0) {
     abort_word = 0;
     for (int s = 0; s < NS; ++s) {
       mbar_init(&full[s], 33);    // the producer's expect_tx arrival and its 32 lanes' scale copies
-      mbar_init(&empty[s], 1);
+      mbar_init(&empty[s], 2);    // the stage's P V products, and the V warp (which a stage without copies needs)
+      mbar_init(&v_go[s], 1);
     }
-    mbar_init(&s_full[0], 1);
-    mbar_init(&s_full[1], 1);
-    mbar_init(p_ready, kQ8SoftmaxWarps);
-    mbar_init(o_full, 1);
-    mbar_init(q_ready, kQ8SoftmaxWarps);
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&s_full[i], 1);
+      mbar_init(&s_free[i], kQ8SoftmaxWarps);
+      mbar_init(&p_ready[i], kQ8SoftmaxWarps);
+      mbar_init(&o_full[i], 1);
+      mbar_init(&q_ready[i], 1);
+    }
     mbar_init(ml_ready, kQ8SoftmaxWarps);
-    mbar_init(done, 1);
+    mbar_init(&done[0], 1);
+    mbar_init(&done[1], 1);
     fence_mbar_init();
   }
   // digit rows that no query head uses stay zero
-  for (int i = threadIdx.x * 16; i < L::kQTile; i += kQ8Threads * 16)
+  for (int i = threadIdx.x * 16; i < 2 * L::kQTile; i += kQ8Threads * 16)
     *reinterpret_cast<uint4*>(smem + L::kQT + i) = make_uint4(0, 0, 0, 0);
-  for (int i = threadIdx.x * 16; i < L::kPTile; i += kQ8Threads * 16)
+  for (int i = threadIdx.x * 16; i < 2 * L::kPTile; i += kQ8Threads * 16)
     *reinterpret_cast<uint4*>(smem + L::kPT + i) = make_uint4(0, 0, 0, 0);
   fence_proxy_async_smem();
-  if (warp == kQ8SoftmaxWarps + 1) {
+  // tiles of each scan entry's share of the sequences, summed by four threads. (A sum fits an int: sequences of
+  // 2^30 tokens would need block tables of terabytes first.)
+  const int per_entry = (p.num_seqs + kQ8Scan - 1) / kQ8Scan;
+  {
+    int sum = 0;
+    const int s0 = (threadIdx.x >> 2) * per_entry;
+    for (int i = threadIdx.x & 3; i < per_entry && s0 + i < p.num_seqs; i += 4) {
+      const int len = __ldg(&p.seq_lens[s0 + i]);
+      if (blockIdx.x == 0 && (len < 0 || len > capacity)) raise_status(p.status, ATTN_ERR_DEVICE_BOUNDS);
+      sum += q8_tiles(q8_clamp_len(len, capacity));
+    }
+    sum += __shfl_xor_sync(0xffffffffu, sum, 1);
+    sum += __shfl_xor_sync(0xffffffffu, sum, 2);
+    if ((threadIdx.x & 3) == 0) scan[threadIdx.x >> 2] = sum;
+  }
+  if (warp == kQ8ScoreWarp) {
     tmem_alloc(&tmem_slot, L::kTmemCols);
     tmem_relinquish();
   }
@@ -278,97 +341,151 @@ __global__ void __launch_bounds__(kQ8Threads, DecodeQ8Smem<D, GP, I8>::kBlocks)
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = tmem_slot;
-  const uint32_t tmem_s = tmem;                 // two buffers of KN columns
-  const uint32_t tmem_o = tmem + 2 * KN;        // four groups of KN columns, one per softmax warp
+  const uint32_t tmem_s = tmem;                    // two buffers of kSBuf columns
+  const uint32_t tmem_o = tmem + 2 * L::kSBuf;     // two buffers of four groups of KN columns, one per softmax warp
 
-  if (warp == kQ8SoftmaxWarps) {
-    // ------------------------------------------------------------ producer warp
-    if (lane == 0) {
-      tma_prefetch_desc(&tm_k);
-      tma_prefetch_desc(&tm_v);
+  if (warp == kQ8KWarp) {
+    // ------------------------------------------------------------ producer warp: work, K, scales
+    if (lane == 0) tma_prefetch_desc(&tm_k);
+    const int c = lane & 7;            // lane: chunk c of the tile; bit 3: V scales; bit 4: second head of the row
+    const bool box_lane = lane < 8 && (c & (p.box / kQ8Chunk - 1)) == 0;   // lane of a copy's first chunk
+    const float* sc_src = (lane & 8) ? p.v_scales : p.k_scales;
+    const int blocks_per_page = p.page_size >> p.block_shift;
+    const int team = int(blockIdx.x) / p.team;
+    const int team_lane = int(blockIdx.x) % p.team;
+
+    // ---- this team's run of the batch's tiles, and the sequence where it starts
+    const long long mine = (long long)scan[2 * lane] + scan[2 * lane + 1];
+    long long incl = mine;
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+      const long long up = __shfl_up_sync(0xffffffffu, incl, d);
+      if (lane >= d) incl += up;
     }
-    const int c = lane & 7;            // lanes 0 .. 7 copy K chunk c, lanes 8 .. 15 V chunk c
-    const bool is_v = lane >= 8;
-    const CUtensorMap* map = is_v ? &tm_v : &tm_k;
-    const float* sc_src = is_v ? qp.v_scales : qp.k_scales;
-    const int blocks_per_page = p.page_size >> qp.block_shift;
+    const long long per_group = __shfl_sync(0xffffffffu, incl, 31);
+    const long long total = per_group * p.groups;
+    // at least two tiles for each team (so no team without one between two parts): a cut costs as much as a tile
+    const int teams = int(min((total + 1) / 2, (long long)p.teams));
+    long long pos = team < teams ? total * team / teams : 0;
+    const long long begin = pos, end = team < teams ? total * (team + 1) / teams : 0;
+    int grp = 0, seq = 0, a = 0;       // next tile: tile a of (group, sequence)
+    int win = -1, win_len = 0;         // lengths of sequences 32 win .. 32 win + 31, one per lane
+    auto len_at = [&](int s) -> int {
+      if ((s >> 5) != win) {
+        win = s >> 5;
+        const int i = win * 32 + lane;
+        win_len = i < p.num_seqs ? q8_clamp_len(__ldg(&p.seq_lens[i]), capacity) : 0;
+      }
+      return __shfl_sync(0xffffffffu, win_len, s & 31);
+    };
+    if (begin < end) {
+      grp = int(begin / per_group);
+      long long x = begin - grp * per_group;
+      const uint32_t at = __ballot_sync(0xffffffffu, incl > x);   // not empty: x < per_group
+      const int l0 = __ffs(int(at)) - 1;
+      x -= __shfl_sync(0xffffffffu, incl - mine, l0);
+      int t = 2 * l0;
+      if (x >= scan[t]) x -= scan[t++];
+      seq = t * per_entry;
+      for (;; ++seq) {
+        const int tiles = q8_tiles(len_at(seq));
+        if (x < tiles) break;
+        x -= tiles;
+      }
+      a = int(x);
+    }
+    // the next part (a run of tiles of one sequence) is taken one part ahead, its first pages requested
+    struct Part { int seq, grp, a, n, len, tiles; long long pos; };
+    Part nx{};
+    int nx_page = -1;
+    auto page_of = [&](int s, int t0) -> int {   // physical page of chunk c of the tile at t0
+      const int e = (t0 + c * kQ8Chunk) >> p.page_shift;
+      return e < p.max_pages ? __ldg(&p.block_table[size_t(s) * p.max_pages + e]) : -1;
+    };
+    auto next_part = [&]() {
+      nx.n = 0;
+      if (pos >= end) return;
+      int len, tiles;
+      for (;;) {
+        if (seq == p.num_seqs) { seq = 0; ++grp; }
+        len = len_at(seq);
+        tiles = q8_tiles(len);
+        if (tiles > a) break;
+        ++seq;
+        a = 0;
+      }
+      const long long left = end - pos;
+      nx.seq = seq; nx.grp = grp; nx.a = a; nx.len = len; nx.tiles = tiles; nx.pos = pos;
+      nx.n = tiles - a < left ? tiles - a : int(left);
+      nx_page = page_of(seq, a * kQ8Tok);
+      pos += nx.n;
+      a += nx.n;
+      if (a == tiles) { a = 0; ++seq; }
+    };
+    next_part();
+    int4 cut = make_int4(-1, 0, 0, 0);
     int slot = 0;
     uint32_t phase = 0;
     uint32_t pending = 0, pending_phase = 0;
     bool ok = true;
-    long long nx_item = 0;
-    int nx_len = 0, nx_page = -1;
-    bool first_fetch = true;
-    auto page_of = [&](int seq, int t0) -> int {   // physical page of chunk c of the tile at t0
-      const int e = (t0 + c * kQ8Chunk) >> qp.page_shift;
-      return e < p.max_pages ? __ldg(&p.block_table[size_t(seq) * p.max_pages + e]) : -1;
-    };
-    auto fetch_next = [&]() {   // next item, its length and its first tile's pages, one item ahead
-      long long t = 0;
-      if (p.static_items) {
-        t = first_fetch ? (long long)blockIdx.x : num_items;
-      } else {
-        if (lane == 0) t = atomicAdd(ticket_counter, 1);
-        t = __shfl_sync(0xffffffffu, t, 0);
-      }
-      first_fetch = false;
-      nx_item = t;
-      if (t < num_items) {
-        const long long per = (long long)p.num_seqs * p.Hkv;
-        const int sp = int(t / per), sq = int(t % per) / p.Hkv;
-        nx_len = __ldg(&p.seq_lens[sq]);
-        nx_page = page_of(sq, sp * p.split_tokens);
-      }
-    };
-    fetch_next();
-    while (ok) {
-      const long long item = nx_item;
-      if (item >= num_items) break;
-      int len = nx_len;
+    while (ok && nx.n > 0) {
+      const Part w = nx;
       int page = nx_page;
-      fetch_next();
-      const long long per = (long long)p.num_seqs * p.Hkv;   // splits outermost: full-length splits go first
-      const int split = int(item / per), rem = int(item % per);
-      const int seq = rem / p.Hkv, kvh = rem % p.Hkv;
-      if (len > capacity || len < 0) {
-        if (lane == 0 && split == 0 && kvh == 0) raise_status(p.status, ATTN_ERR_DEVICE_BOUNDS);
-        len = len < 0 ? 0 : capacity;
+      next_part();
+      const int row = w.grp * p.team + team_lane;      // 128-byte row of the tokens
+      if (row >= p.rows128) continue;                  // a lane past the last row
+      const bool whole = w.n == w.tiles;
+      const int part = whole ? -1 : int(blockIdx.x) * 2 + (w.pos == begin ? 0 : 1);
+      if (!whole && w.a == 0) {   // the first part of a cut sequence: this CTA's last work
+        const long long last = w.pos + w.tiles - 1;    // the team of its last tile
+        cut = make_int4(w.seq, w.grp, int(((last + 1) * teams - 1) / total), part & 1);
       }
-      const int t_begin = split * p.split_tokens;
-      if (t_begin >= len) continue;
-      const int t_end = min(t_begin + p.split_tokens, len);
+      const int head0 = NH == 2 ? row * 2 : row;       // first KV head of the row's query rows
+      const int head = head0 + (NH == 2 ? lane >> 4 : 0);
+      const bool head_ok = head < p.Hkv && (NH == 2 || lane < 16);
+      const int byte = (p.solo ? row >> 1 : row) * kQ8Row;
+      const int q_rows = min(NH * p.G, p.Hq - head0 * p.G);
+      const int t_begin = w.a * kQ8Tok, t_end = min((w.a + w.n) * kQ8Tok, w.len);
       for (int t0 = t_begin; t0 < t_end && ok; t0 += kQ8Tok) {
-        const int page_next = t0 + kQ8Tok < t_end ? page_of(seq, t0 + kQ8Tok) : -1;
-        if (!__all_sync(0xffffffffu, mbar_wait(&empty[slot], phase ^ 1u, abort_flag, p.status))) { ok = false; break; }
+        const int page_next = t0 + kQ8Tok < t_end ? page_of(w.seq, t0 + kQ8Tok) : -1;
         const int ntok = min(kQ8Tok, t_end - t0);
         const bool in_range = page >= 0 && page < p.num_pages;
-        const bool good = lane < 16 && c * kQ8Chunk < ntok && in_range;
+        const bool held = c * kQ8Chunk < ntok;
+        const bool good = held && in_range;
         const uint32_t good_mask = __ballot_sync(0xffffffffu, good) & 0xFFu;
-        const bool outside = __any_sync(0xffffffffu, lane < 8 && c * kQ8Chunk < ntok && !in_range);
+        const uint32_t box_mask = __ballot_sync(0xffffffffu, good && box_lane);   // copies to issue
+        if (__any_sync(0xffffffffu, held && !in_range) && lane == 0) raise_status(p.status, ATTN_ERR_DEVICE_BOUNDS);
+        const int in_page = (t0 + c * kQ8Chunk) & (p.page_size - 1);
+        const bool copy_scale = good && head_ok;
+        const float* sc = sc_src + (copy_scale ? (size_t(page) * blocks_per_page + (in_page >> p.block_shift)) * p.Hkv + head
+                                               : size_t(0));
+        const bool first = t0 == t_begin;
         uint8_t* stage = smem + slot * L::kStageBytes;
+        int* job = reinterpret_cast<int*>(smem + L::kJob) + slot * 12;
+        if (!__all_sync(0xffffffffu, mbar_wait(&empty[slot], phase ^ 1u, abort_flag, p.status))) { ok = false; break; }
+        if (lane < 8) job[lane] = page;
         if (lane == 0) {
-          if (outside) raise_status(p.status, ATTN_ERR_DEVICE_BOUNDS);
-          const bool first = t0 == t_begin;
+          job[8] = t0;
+          job[9] = byte;
+          job[10] = int(box_mask);
           TileInfo ti;
-          ti.seq = seq; ti.split = split; ti.kvh = kvh; ti.t0 = t0;
+          ti.seq = w.seq; ti.split = part; ti.kvh = row; ti.t0 = t0;
           ti.ntok = ntok;
           ti.bad = int(~good_mask & 0xFFu);
           ti.flags = (first ? 1 : 0) | (t0 + kQ8Tok >= t_end ? 2 : 0);
-          ti.len = len;
+          ti.len = w.len;
           info[slot] = ti;
-          const uint32_t qbytes = first ? uint32_t(qp.G * D * 2) : 0u;
-          mbar_arrive_expect_tx(&full[slot], uint32_t(__popc(good_mask)) * uint32_t(2 * kQ8Chunk * D) + qbytes);
+          const uint32_t qbytes = first ? uint32_t(q_rows * D * 2) : 0u;
+          mbar_arrive_expect_tx(&full[slot], uint32_t(__popc(box_mask)) * uint32_t(2 * kQ8Row * p.box) + qbytes);
           if (first)
-            bulk_load(stage + 2 * L::kTileBytes, p.q + (size_t(seq) * p.Hq + size_t(kvh) * qp.G) * D, qbytes,
+            bulk_load(smem + L::kQRows + slot * L::kQBytes, p.q + (size_t(w.seq) * p.Hq + size_t(head0) * p.G) * D, qbytes,
                       &full[slot]);
         }
         __syncwarp();
-        if (good) {
-          const int in_page = (t0 + c * kQ8Chunk) & (p.page_size - 1);
-          tma_load_4d(stage + (is_v ? L::kTileBytes : 0) + c * (kQ8Chunk * D), map, &full[slot], 0, in_page, kvh, page);
-          cp_async4(scales + slot * 16 + lane,
-                    sc_src + (size_t(page) * blocks_per_page + (in_page >> qp.block_shift)) * p.Hkv + kvh);
-        }
+        if (lane == 0) mbar_arrive(&v_go[slot]);
+        if ((box_mask >> lane) & 1)
+          tma_load_3d(stage + c * (kQ8Chunk * kQ8Row), &tm_k, &full[slot], byte, in_page, page);
+        if (copy_scale) cp_async4(scales + slot * 16 * NH + lane, sc);
         cp_async_arrive_noinc(&full[slot]);
         __syncwarp();
         pending |= 1u << slot;
@@ -377,12 +494,15 @@ __global__ void __launch_bounds__(kQ8Threads, DecodeQ8Smem<D, GP, I8>::kBlocks)
         page = page_next;
       }
     }
+    if (lane == 0) p.ws_cut[blockIdx.x] = cut;
     if (ok && __all_sync(0xffffffffu, mbar_wait(&empty[slot], phase ^ 1u, abort_flag, p.status))) {
       if (lane == 0) {   // end-of-work marker: a stage with no copies
         TileInfo ti{};
         ti.flags = 4;
         info[slot] = ti;
+        reinterpret_cast<int*>(smem + L::kJob)[slot * 12 + 10] = -1;
         mbar_arrive_expect_tx(&full[slot], 0u);
+        mbar_arrive(&v_go[slot]);
       }
       __syncwarp();
       cp_async_arrive_noinc(&full[slot]);
@@ -394,247 +514,283 @@ __global__ void __launch_bounds__(kQ8Threads, DecodeQ8Smem<D, GP, I8>::kBlocks)
       for (int s = 0; s < NS; ++s)
         if (pending & (1u << s)) mbar_drain(&full[s], (pending_phase >> s) & 1u);
     }
-  } else if (warp == kQ8SoftmaxWarps + 1) {
-    // ------------------------------------------------------------ MMA warp (one thread)
+  } else if (warp == kQ8VWarp) {
+    // ------------------------------------------------------------ producer warp: V, as the first one says
+    if (lane == 0) tma_prefetch_desc(&tm_v);
+    int slot = 0;
+    uint32_t phase = 0;
+    while (__all_sync(0xffffffffu, mbar_wait(&v_go[slot], phase, abort_flag, p.status))) {
+      const int* job = reinterpret_cast<const int*>(smem + L::kJob) + slot * 12;
+      const int mask = job[10];
+      if (mask < 0) break;   // end of work
+      if (lane < 8 && ((mask >> lane) & 1)) {
+        const int in_page = (job[8] + lane * kQ8Chunk) & (p.page_size - 1);
+        tma_load_3d(smem + slot * L::kStageBytes + L::kTileBytes + lane * (kQ8Chunk * kQ8Row), &tm_v, &full[slot], job[9],
+                    in_page, job[lane]);
+      }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&empty[slot]);
+      if (++slot == NS) { slot = 0; phase ^= 1u; }
+    }
+  } else if (warp == kQ8ScoreWarp) {
+    // ------------------------------------------------------------ query digits and score products
+    constexpr uint32_t idesc_s = make_idesc_q8<I8>(kQ8Tok, KN, 0);   // K tile: rows = tokens, K-major
+    const uint64_t q_desc0 = make_sdesc_rows(smem_u32(smem + L::kQT));
+    const uint64_t k_desc0 = make_sdesc_rows(smem_u32(smem));
+    int slot = 0, sb = 0, qb = 1;
+    uint32_t phase = 0, f_ph = 1;   // a fresh s_free lets the first two tiles pass
+    while (__all_sync(0xffffffffu, mbar_wait(&full[slot], phase, abort_flag, p.status))) {
+      const int flags = info[slot].flags, row = info[slot].kvh;
+      if (flags & 4) break;
+      if (!__all_sync(0xffffffffu, mbar_wait(&s_free[sb], f_ph, abort_flag, p.status))) break;
+      const int half = D == 64 && NH == 1 ? row & 1 : 0;   // solo: the head's half of the row
+      if (flags & 1) {
+        // the item's query rows as digits, scaled by a power of two (exact). The buffer's last reader, the
+        // item before the previous one, is done: the scores of the tile two before this one have been read
+        qb ^= 1;
+        uint8_t* q_tile = smem + L::kQT + qb * L::kQTile;
+        float* qf = reinterpret_cast<float*>(smem + L::kQf) + qb * R;
+        const int head0 = NH == 2 ? row * 2 : row;
+        for (int i = 0; i < NH * p.G; ++i) {
+          const int nh = NH == 2 && i >= p.G ? 1 : 0;
+          if (head0 + nh >= p.Hkv) break;
+          const int r = nh * GP + (i - nh * p.G);            // digit row
+          constexpr int E = D / 32;   // values per lane
+          const uint32_t* src =
+              reinterpret_cast<const uint32_t*>(smem + L::kQRows + slot * L::kQBytes + i * D * 2) + lane * (E / 2);
+          uint32_t w[E / 2];
+          uint32_t top = 0;
+#pragma unroll
+          for (int k = 0; k < E / 2; ++k) {
+            w[k] = src[k];
+            top = max(top, max((w[k] << 16) & 0x7FFF0000u, w[k] & 0x7FFF0000u));
+          }
+          top = __reduce_max_sync(0xffffffffu, top);
+          const int e = int(top >> 23) - 127, mant = int(top >> 16) & 0x7F;
+          const bool finite = top < 0x7F800000u;
+          // the largest value lands in (224, 448] or [16320, 32639]
+          int sh = I8 ? 14 - e - (mant == 0x7F ? 1 : 0) : 8 - e - (mant > 0x60 ? 1 : 0);
+          sh = min(sh, 118);
+          const float up = finite ? __uint_as_float(uint32_t(sh + 127) << 23) : 0.f;
+          if (lane == 0)
+            qf[r] = finite ? p.scale_log2 * __uint_as_float(uint32_t(127 - sh) << 23) : __int_as_float(0x7fc00000);
+#pragma unroll
+          for (int k = 0; k < E / 2; ++k) {
+            uint32_t hi = 0, lo = 0;
+            if (finite) two_digits<I8>(bf16_lo(w[k]) * up, bf16_hi(w[k]) * up, hi, lo);
+            const int byte = (half + nh) * 64 + lane * E + 2 * k;
+            *reinterpret_cast<uint16_t*>(q_tile + row_unit(r, byte >> 4) + (byte & 15)) = uint16_t(hi);
+            *reinterpret_cast<uint16_t*>(q_tile + row_unit(R + r, byte >> 4) + (byte & 15)) = uint16_t(lo);
+          }
+        }
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&q_ready[qb]);
+      }
+      if (lane == 0) {
+        tc_fence_after();
+        const uint64_t k_desc = k_desc0 + uint64_t(slot * (L::kStageBytes >> 4)) + (D == 64 && NH == 1 ? 4 * half : 0);
+        const uint64_t q_desc = q_desc0 + uint64_t(qb * (L::kQTile >> 4)) + (D == 64 && NH == 1 ? 4 * half : 0);
+        // each head's products run over its own bytes of the row alone, so that a NaN code of one head does
+        // not reach the other's scores
+#pragma unroll
+        for (int h = 0; h < NH; ++h)
+#pragma unroll
+          for (int k = 0; k < D / 32; ++k)
+            umma_q8<I8>(tmem_s + sb * L::kSBuf + h * KN, k_desc + 2 * (h * (D / 32) + k), q_desc + 2 * (h * (D / 32) + k),
+                        idesc_s, k > 0);
+        umma_commit(&s_full[sb]);
+      }
+      __syncwarp();
+      if (++slot == NS) { slot = 0; phase ^= 1u; }
+      if (sb) f_ph ^= 1u;
+      sb ^= 1;
+    }
     if (lane == 0) {
-      constexpr uint32_t idesc_s = make_idesc_q8<I8>(kQ8Tok, KN, 0);   // K tile: rows = tokens, K-major
-      constexpr uint32_t idesc_o = make_idesc_q8<I8>(D, KN, 1);        // V tile: rows = head dims, MN-major
-      const uint64_t q_desc = make_sdesc_rows<D>(smem_u32(smem + L::kQT));
-      const uint64_t p_desc = make_sdesc_rows<128>(smem_u32(smem + L::kPT));
-      int slot = 0, sb = 0;
-      uint32_t phase = 0, p_ph = 0, q_ph = 0;
-      auto issue_s = [&](int s, int b) {   // S^T of stage s into buffer b
-        const uint64_t k_desc = make_sdesc_rows<D>(smem_u32(smem + s * L::kStageBytes));
-#pragma unroll
-        for (int k = 0; k < D / 32; ++k)
-          umma_q8<I8>(tmem_s + b * KN, k_desc + 2 * k, q_desc + 2 * k, idesc_s, k > 0);
-        umma_commit(&s_full[b]);
-      };
-      bool ok = mbar_wait(&full[0], 0, abort_flag, p.status);
-      bool live = ok && !(info[0].flags & 4);
-      if (live) {
-        ok = mbar_wait(q_ready, q_ph, abort_flag, p.status);
-        q_ph ^= 1u;
+      umma_commit(&done[0]);   // nothing of this thread is in flight when TMEM is given back
+      mbar_drain(&done[0], 0);
+    }
+    __syncwarp();
+  } else if (warp == kQ8PvWarp) {
+    // ------------------------------------------------------------ P V products (one thread)
+    if (lane == 0) {
+      constexpr uint32_t idesc_o = make_idesc_q8<I8>(kQ8Row, KN, 1);   // V tile: rows = head dims, MN-major
+      const uint64_t p_desc0 = make_sdesc_rows(smem_u32(smem + L::kPT));
+      const uint64_t v_desc0 = make_sdesc_rows(smem_u32(smem + L::kTileBytes));
+      int slot = 0, pb = 0;
+      uint32_t phase = 0, p_ph = 0;
+      while (mbar_wait(&full[slot], phase, abort_flag, p.status)) {
+        if (info[slot].flags & 4) break;
+        if (!mbar_wait(&p_ready[pb], p_ph, abort_flag, p.status)) break;
         tc_fence_after();
-        if (ok) issue_s(0, 0);
-      }
-      while (ok && live) {
-        const int ns = slot + 1 == NS ? 0 : slot + 1;
-        const uint32_t nph = ns == 0 ? phase ^ 1u : phase;
-        bool issued = false, seen = false;
-        int nflags = 0;
-        // the next tile's scores while this tile's softmax runs, unless it needs a new query
-        const unsigned long long t_start = global_timer_ns();
-        for (uint32_t i = 1; !mbar_test_wait(p_ready, p_ph); ++i) {
-          if (!seen && mbar_test_wait(&full[ns], nph)) {
-            seen = true;
-            nflags = info[ns].flags;
-            if (!(nflags & 5)) {
-              tc_fence_after();
-              issue_s(ns, sb ^ 1);
-              issued = true;
-            }
-          }
-          if ((i & 63u) == 0) {
-            if (*abort_flag) { ok = false; break; }
-            if (global_timer_ns() - t_start > kWaitLimitNs) {
-              *abort_flag = 1;
-              raise_status(p.status, ATTN_ERR_TIMEOUT);
-              ok = false;
-              break;
-            }
-          }
-        }
-        if (!ok) break;
-        p_ph ^= 1u;
-        tc_fence_after();
-        // O^T_w of this tile: tokens 32w .. 32w + 31
+        const uint64_t v_desc = v_desc0 + uint64_t(slot * (L::kStageBytes >> 4));
+        const uint64_t p_desc = p_desc0 + uint64_t(pb * (L::kPTile >> 4));
 #pragma unroll
-        for (int w = 0; w < 4; ++w) {
-          const uint64_t v_desc =
-              make_sdesc_rows<D>(smem_u32(smem + slot * L::kStageBytes + L::kTileBytes + w * 32 * D));
-          umma_q8<I8>(tmem_o + w * KN, v_desc, p_desc + 2 * w, idesc_o, 0);
-        }
-        umma_commit(o_full);
-        umma_commit(&empty[slot]);
-        if (!seen) {
-          if (!mbar_wait(&full[ns], nph, abort_flag, p.status)) { ok = false; break; }
-          nflags = info[ns].flags;
-        }
-        if (nflags & 4) break;
-        if (!issued) {
-          if (nflags & 1) {
-            if (!mbar_wait(q_ready, q_ph, abort_flag, p.status)) { ok = false; break; }
-            q_ph ^= 1u;
-          }
-          tc_fence_after();
-          issue_s(ns, sb ^ 1);
-        }
-        slot = ns;
-        phase = nph;
-        sb ^= 1;
+        for (int w = 0; w < 4; ++w)   // O^T_w: tokens 32w .. 32w + 31
+          umma_q8<I8>(tmem_o + (pb * 4 + w) * KN, v_desc + uint64_t(w * (32 * kQ8Row >> 4)), p_desc + 2 * w, idesc_o, 0);
+        umma_commit(&o_full[pb]);
+        umma_commit(&empty[slot]);    // the tile's products are done with its K and V
+        if (++slot == NS) { slot = 0; phase ^= 1u; }
+        if (pb) p_ph ^= 1u;
+        pb ^= 1;
       }
-      umma_commit(done);       // nothing of this thread is in flight when TMEM is given back
-      mbar_drain(done, 0);
+      umma_commit(&done[1]);
+      mbar_drain(&done[1], 0);
     }
     __syncwarp();
   } else {
     // ------------------------------------------------------------ softmax warps: thread = token, then head dim
     const float neg_inf = -__int_as_float(0x7f800000);
     const uint32_t lane_base = uint32_t(warp * 32) << 16;
-    const int tok = warp * 32 + lane;
-    const int dim = D == 128 ? tok : warp * 16 + lane;   // M = 64: rows 16w .. 16w + 15 sit in lanes 32w ..
-    const bool dim_valid = D == 128 || lane < 16;
+    const int tok = warp * 32 + lane;         // also the byte of the row whose O this thread holds
+    const int my_half = NH == 2 ? warp >> 1 : 0;
     float* alpha = reinterpret_cast<float*>(smem + L::kAlpha);
     float* ml = reinterpret_cast<float*>(smem + L::kMl);
-    float* qf_s = reinterpret_cast<float*>(smem + L::kQf);
-    uint8_t* p_tile = smem + L::kPT;
+    const float* qf_s = reinterpret_cast<const float*>(smem + L::kQf);
     constexpr float kPScale = I8 ? 32512.f : 256.f;   // 127 * 256: both digits stay inside int8
-    int slot = 0, sb = 0;
-    uint32_t phase = 0, s_ph = 0, p_ph = 0, o_ph = 0, q_ph = 0, m_ph = 0;
+    int slot = 0, tile = 0, item_no = 0;
+    uint32_t phase = 0, m_ph = 0;
     bool ok = true;
-    int seq = 0, split = 0, kvh = 0, n_splits = 0;
-    float qf[GP], X[GP], Y[GP], l[GP];
+    int seq = 0, part = 0, row = 0;
+    float qf[R], X[R], Y[R], l[R];
     float o[4][GP];
 #pragma unroll
-    for (int h = 0; h < GP; ++h) {
-      qf[h] = 0.f; X[h] = Y[h] = neg_inf; l[h] = 0.f;
-      o[0][h] = o[1][h] = o[2][h] = o[3][h] = 0.f;
-    }
+    for (int h = 0; h < R; ++h) { qf[h] = 0.f; X[h] = Y[h] = neg_inf; l[h] = 0.f; }
+#pragma unroll
+    for (int h = 0; h < GP; ++h) o[0][h] = o[1][h] = o[2][h] = o[3][h] = 0.f;
     auto wait = [&](uint64_t* bar, uint32_t ph) -> bool {   // the same answer in the whole warp
       return __all_sync(0xffffffffu, mbar_wait(bar, ph, abort_flag, p.status));
     };
+    // O^T of tile number t: thread = head dimension, one accumulator per warp's tokens
+    auto add_tile = [&](int t) -> bool {
+      const int b = t & 1;
+      const uint32_t ph = uint32_t(t >> 1) & 1u;
+      if (!wait(&p_ready[b], ph) || !wait(&o_full[b], ph)) return false;   // every warp's factors; the products
+      tc_fence_after();
+      const float* al = alpha + (t & 3) * 4 * R + my_half * GP;
+      constexpr int WB = GP <= 4 ? 4 : 2;   // accumulator groups read together
+#pragma unroll
+      for (int w0 = 0; w0 < 4; w0 += WB) {
+        uint32_t hi[WB][GP], lo[WB][GP];
+#pragma unroll
+        for (int w = 0; w < WB; ++w) {
+          const uint32_t at = tmem_o + (b * 4 + w0 + w) * KN + lane_base + my_half * GP;
+          tmem_ld_cols<GP>(at, hi[w]);
+          tmem_ld_cols<GP>(at + R, lo[w]);
+        }
+        tmem_ld_wait();
+#pragma unroll
+        for (int w = 0; w < WB; ++w) {
+          reg_fence<GP>(hi[w]);
+          reg_fence<GP>(lo[w]);
+#pragma unroll
+          for (int h = 0; h < GP; ++h)
+            o[w0 + w][h] = fmaf(o[w0 + w][h], al[(w0 + w) * R + h], join_digits<I8>(hi[w][h], lo[w][h]));
+        }
+      }
+      tc_fence_before();
+      return true;
+    };
 
     while (ok) {
+      const int sb = tile & 1;
+      const uint32_t t_ph = uint32_t(tile >> 1) & 1u;   // this tile's use of its double buffers
       if (!wait(&full[slot], phase)) { ok = false; break; }
       const TileInfo ti = info[slot];
       if (ti.flags & 4) break;
       uint8_t* stage = smem + slot * L::kStageBytes;
-      if (ti.flags & 1) {
-        // ---- the item's query rows as digits, scaled by a power of two (exact)
-        seq = ti.seq; split = ti.split; kvh = ti.kvh;
-        n_splits = (ti.len + p.split_tokens - 1) / p.split_tokens;
-        for (int r = warp; r < qp.G; r += kQ8SoftmaxWarps) {
-          constexpr int E = D / 32;   // values per lane
-          const uint32_t* src = reinterpret_cast<const uint32_t*>(stage + 2 * L::kTileBytes + r * D * 2) + lane * (E / 2);
-          uint32_t w[E / 2];
-          uint32_t top = 0;
+      const bool first = (ti.flags & 1) != 0;
+      if (first) {
+        seq = ti.seq; part = ti.split; row = ti.kvh;
+        if (!wait(&q_ready[item_no & 1], uint32_t(item_no >> 1) & 1u)) { ok = false; break; }
+        const float* qs = qf_s + (item_no & 1) * R;
 #pragma unroll
-          for (int i = 0; i < E / 2; ++i) {
-            w[i] = src[i];
-            top = max(top, max((w[i] << 16) & 0x7FFF0000u, w[i] & 0x7FFF0000u));
-          }
-          top = __reduce_max_sync(0xffffffffu, top);
-          const int e = int(top >> 23) - 127, mant = int(top >> 16) & 0x7F;
-          const bool finite = top < 0x7F800000u;
-          // the largest value lands in (224, 448] or [16320, 32639]
-          int a = I8 ? 14 - e - (mant == 0x7F ? 1 : 0) : 8 - e - (mant > 0x60 ? 1 : 0);
-          a = min(a, 118);
-          const float up = finite ? __uint_as_float(uint32_t(a + 127) << 23) : 0.f;
-          if (lane == 0)
-            qf_s[r] = finite ? p.scale_log2 * __uint_as_float(uint32_t(127 - a) << 23) : __int_as_float(0x7fc00000);
-#pragma unroll
-          for (int i = 0; i < E / 2; ++i) {
-            uint32_t hi = 0, lo = 0;
-            if (finite) two_digits<I8>(bf16_lo(w[i]) * up, bf16_hi(w[i]) * up, hi, lo);
-            const int byte = lane * E + 2 * i;
-            uint8_t* q_tile = smem + L::kQT;
-            *reinterpret_cast<uint16_t*>(q_tile + row_unit<D>(r, byte >> 4) + (byte & 15)) = uint16_t(hi);
-            *reinterpret_cast<uint16_t*>(q_tile + row_unit<D>(GP + r, byte >> 4) + (byte & 15)) = uint16_t(lo);
-          }
-        }
-        fence_proxy_async_smem();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(q_ready);
-        if (!wait(q_ready, q_ph)) { ok = false; break; }
-        q_ph ^= 1u;
-#pragma unroll
-        for (int h = 0; h < GP; ++h) {
-          qf[h] = h < qp.G ? qf_s[h] : 0.f;
+        for (int h = 0; h < R; ++h) {
+          qf[h] = h % GP < p.G ? qs[h] : 0.f;
           X[h] = Y[h] = neg_inf;
           l[h] = 0.f;
-          o[0][h] = o[1][h] = o[2][h] = o[3][h] = 0.f;
         }
+#pragma unroll
+        for (int h = 0; h < GP; ++h) o[0][h] = o[1][h] = o[2][h] = o[3][h] = 0.f;
+        ++item_no;
       }
       const bool last = (ti.flags & 2) != 0;
       const bool valid = tok < ti.ntok && !((ti.bad >> (tok >> 4)) & 1);
       if (!valid) {   // a V row that was not copied: 0 * (stale bytes) must not reach O
-        uint4* row = reinterpret_cast<uint4*>(stage + L::kTileBytes + tok * D);
+        uint4* v_row = reinterpret_cast<uint4*>(stage + L::kTileBytes + tok * kQ8Row);
 #pragma unroll
-        for (int i = 0; i < D / 16; ++i) row[i] = make_uint4(0, 0, 0, 0);
+        for (int i = 0; i < kQ8Row / 16; ++i) v_row[i] = make_uint4(0, 0, 0, 0);
       }
-      const float ks = scales[slot * 16 + (tok >> 4)];
-      const float lvs = __log2f(scales[slot * 16 + 8 + (tok >> 4)]);
+      float ks[NH], lvs[NH];
+#pragma unroll
+      for (int n = 0; n < NH; ++n) {
+        ks[n] = scales[slot * 16 * NH + n * 16 + (tok >> 4)];
+        lvs[n] = __log2f(scales[slot * 16 * NH + n * 16 + 8 + (tok >> 4)]);
+      }
 
       // ---- scores of this token for all heads
-      if (!wait(&s_full[sb], s_ph)) { ok = false; break; }
+      if (!wait(&s_full[sb], t_ph)) { ok = false; break; }
       tc_fence_after();
-      uint32_t sr[2 * GP];
-      tmem_ld_cols<2 * GP>(tmem_s + sb * KN + lane_base, sr);
-      tmem_ld_wait();
-      reg_fence<2 * GP>(sr);
-      float pv[GP];
+      uint32_t s_hi[R], s_lo[R];
 #pragma unroll
-      for (int h = 0; h < GP; ++h) {
-        const float x = valid ? join_digits<I8>(sr[h], sr[GP + h]) * (qf[h] * ks) : neg_inf;
-        const float y = valid ? x + lvs : neg_inf;
+      for (int n = 0; n < NH; ++n) {
+        const uint32_t at = tmem_s + sb * L::kSBuf + n * KN + lane_base + n * GP;
+        tmem_ld_cols<GP>(at, s_hi + n * GP);
+        tmem_ld_cols<GP>(at + R, s_lo + n * GP);
+      }
+      tmem_ld_wait();
+      reg_fence<R>(s_hi);
+      reg_fence<R>(s_lo);
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&s_free[sb]);
+      float pv[R];
+#pragma unroll
+      for (int h = 0; h < R; ++h) {
+        const float x = valid ? join_digits<I8>(s_hi[h], s_lo[h]) * (qf[h] * ks[h / GP]) : neg_inf;
+        const float y = valid ? x + lvs[h / GP] : neg_inf;
         const float nx = max_nan(X[h], warp_max_nan(x)), ny = max_nan(Y[h], warp_max_nan(y));
         const float offx = nx == neg_inf ? 0.f : nx, offy = ny == neg_inf ? 0.f : ny;
         l[h] = fmaf(l[h], fast_exp2(X[h] - offx), fast_exp2(x - offx));
         pv[h] = fast_exp2(y - offy) * kPScale;
-        if (lane == 0) alpha[(sb * 4 + warp) * GP + h] = fast_exp2(Y[h] - offy);
+        if (lane == 0) alpha[((tile & 3) * 4 + warp) * R + h] = fast_exp2(Y[h] - offy);
         X[h] = nx;
         Y[h] = ny;
       }
-      // ---- P digits: row h (hi) and GP + h (lo), this token's byte
+      // ---- P digits: row h (hi) and R + h (lo), this token's byte
       {
+        uint8_t* p_tile = smem + L::kPT + sb * L::kPTile;
         const int unit = 2 * warp + (lane >> 4), b = lane & 15;
 #pragma unroll
-        for (int h = 0; h < GP; h += 2) {
+        for (int h = 0; h < R; h += 2) {
           uint32_t hi, lo;
-          two_digits<I8>(pv[h], h + 1 < GP ? pv[h + 1 < GP ? h + 1 : h] : 0.f, hi, lo);
-          p_tile[row_unit<128>(h, unit) + b] = uint8_t(hi);
-          p_tile[row_unit<128>(GP + h, unit) + b] = uint8_t(lo);
-          if (h + 1 < GP) {
-            p_tile[row_unit<128>(h + 1, unit) + b] = uint8_t(hi >> 8);
-            p_tile[row_unit<128>(GP + h + 1, unit) + b] = uint8_t(lo >> 8);
+          two_digits<I8>(pv[h], h + 1 < R ? pv[h + 1 < R ? h + 1 : h] : 0.f, hi, lo);
+          p_tile[row_unit(h, unit) + b] = uint8_t(hi);
+          p_tile[row_unit(R + h, unit) + b] = uint8_t(lo);
+          if (h + 1 < R) {
+            p_tile[row_unit(h + 1, unit) + b] = uint8_t(hi >> 8);
+            p_tile[row_unit(R + h + 1, unit) + b] = uint8_t(lo >> 8);
           }
         }
       }
       fence_proxy_async_smem();
       tc_fence_before();
       __syncwarp();
-      if (lane == 0) mbar_arrive(p_ready);
+      if (lane == 0) mbar_arrive(&p_ready[sb]);
 
-      // ---- O of this tile: thread = head dimension, one accumulator per warp's tokens
-      if (!wait(p_ready, p_ph)) { ok = false; break; }   // every warp's factors are in
-      p_ph ^= 1u;
-      if (!wait(o_full, o_ph)) { ok = false; break; }
-      o_ph ^= 1u;
-      tc_fence_after();
-#pragma unroll
-      for (int w = 0; w < 4; ++w) {
-        uint32_t r[2 * GP];
-        tmem_ld_cols<2 * GP>(tmem_o + w * KN + lane_base, r);
-        tmem_ld_wait();
-        reg_fence<2 * GP>(r);
-#pragma unroll
-        for (int h = 0; h < GP; ++h)
-          o[w][h] = fmaf(o[w][h], alpha[(sb * 4 + w) * GP + h], join_digits<I8>(r[h], r[GP + h]));
-      }
-      tc_fence_before();
+      if (!first && !add_tile(tile - 1)) { ok = false; break; }
       if (++slot == NS) { slot = 0; phase ^= 1u; }
-      if (sb) s_ph ^= 1u;
-      sb ^= 1;
+      ++tile;
       if (!last) continue;
+      if (!add_tile(tile - 1)) { ok = false; break; }
 
-      // ---- the item's result: the four warps' accumulators onto common maxima
+      // ---- the part's result: the four warps' accumulators onto common maxima
 #pragma unroll
-      for (int h = 0; h < GP; ++h) {
+      for (int h = 0; h < R; ++h) {
 #pragma unroll
         for (int s = 16; s > 0; s >>= 1) l[h] += __shfl_xor_sync(0xffffffffu, l[h], s);
         if (lane == 0) {
-          float* m = ml + (warp * GP + h) * 3;
+          float* m = ml + (warp * R + h) * 3;
           m[0] = X[h]; m[1] = Y[h]; m[2] = l[h];
         }
       }
@@ -642,34 +798,37 @@ __global__ void __launch_bounds__(kQ8Threads, DecodeQ8Smem<D, GP, I8>::kBlocks)
       if (lane == 0) mbar_arrive(ml_ready);
       if (!wait(ml_ready, m_ph)) { ok = false; break; }
       m_ph ^= 1u;
+      const int head = (NH == 2 ? row * 2 : row) + my_half;   // KV head whose dims this thread may hold
+      const int dim = D == 64 ? tok & 63 : tok;
+      const bool mine = head < p.Hkv && (D == 128 || NH == 2 || (tok >> 6) == (row & 1));
 #pragma unroll
       for (int h = 0; h < GP; ++h) {
-        if (h >= qp.G) continue;
+        if (h >= p.G || !mine) continue;
+        const float* mh = ml + (my_half * GP + h) * 3;
         float mx = neg_inf, my = neg_inf;
 #pragma unroll
         for (int w = 0; w < 4; ++w) {
-          mx = max_nan(mx, ml[(w * GP + h) * 3]);
-          my = max_nan(my, ml[(w * GP + h) * 3 + 1]);
+          mx = max_nan(mx, mh[w * R * 3]);
+          my = max_nan(my, mh[w * R * 3 + 1]);
         }
         const float offx = mx == neg_inf ? 0.f : mx, offy = my == neg_inf ? 0.f : my;
         float lsum = 0.f, acc = 0.f;
 #pragma unroll
         for (int w = 0; w < 4; ++w) {
-          lsum = fmaf(ml[(w * GP + h) * 3 + 2], fast_exp2(ml[(w * GP + h) * 3] - offx), lsum);
-          acc = fmaf(o[w][h], fast_exp2(ml[(w * GP + h) * 3 + 1] - offy), acc);
+          lsum = fmaf(mh[w * R * 3 + 2], fast_exp2(mh[w * R * 3] - offx), lsum);
+          acc = fmaf(o[w][h], fast_exp2(mh[w * R * 3 + 1] - offy), acc);
         }
         // lsum is 0 only if every page was invalid; a NaN stays a NaN
         const float out = lsum == 0.f ? 0.f : acc * fast_exp2(offy - offx) * (1.f / kPScale) / lsum;
         const float lse2 = lsum == 0.f ? neg_inf : mx + __log2f(lsum);
-        const int hq = kvh * qp.G + h;
-        if (n_splits == 1) {
-          if (dim_valid) p.o[(size_t(seq) * p.Hq + hq) * D + dim] = __float2bfloat16_rn(out);
-          if (p.lse && threadIdx.x == 0) p.lse[size_t(seq) * p.Hq + hq] = lse2 * 0.69314718055994531f;
+        if (part < 0) {
+          const size_t at = size_t(seq) * p.Hq + size_t(head) * p.G + h;
+          p.o[at * D + dim] = __float2bfloat16_rn(out);
+          if (p.lse && dim == 0) p.lse[at] = lse2 * 0.69314718055994531f;
         } else {
-          const uint64_t keep = l2_keep_policy();   // the merge reads these back after the KV stream
-          const size_t row = (size_t(seq) * p.max_splits + split) * p.Hq + hq;
-          if (dim_valid) st_keep(p.ws_o + row * D + dim, out, keep);
-          if (threadIdx.x == 0) st_keep(p.ws_lse + row, lse2, keep);
+          const size_t at = size_t(part) * p.part_rows + my_half * p.G + h;
+          p.ws_o[at * D + dim] = out;
+          if (dim == 0) p.ws_lse[at] = lse2;
         }
       }
     }
@@ -677,7 +836,74 @@ __global__ void __launch_bounds__(kQ8Threads, DecodeQ8Smem<D, GP, I8>::kBlocks)
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  if (warp == kQ8SoftmaxWarps + 1) tmem_dealloc(tmem, L::kTmemCols);
+  if (warp == kQ8ScoreWarp) tmem_dealloc(tmem, L::kTmemCols);
+}
+
+// The cut sequences: CTA (i, r) merges query row r of the sequence whose first part split CTA i
+// holds, if it holds one; its other parts are the first ones of the same lane in the following
+// teams. Sequences without tokens are written here too (o = 0, lse = -inf).
+template <int D>
+__global__ void __launch_bounds__(D) decode_q8_merge_kernel(const DecodeQ8Params p) {
+  __shared__ float weight[kQ8MaxCtas], warp_max[D / 32];
+  const float neg_inf = -__int_as_float(0x7f800000);
+  const int d = threadIdx.x;
+  grid_dependency_wait();
+  if (blockIdx.y == 0) {
+    for (int s = blockIdx.x; s < p.num_seqs; s += gridDim.x) {
+      if (__ldg(&p.seq_lens[s]) > 0) continue;
+      for (int h = 0; h < p.Hq; ++h) p.o[(size_t(s) * p.Hq + h) * D + d] = __float2bfloat16_rn(0.f);
+      if (p.lse)
+        for (int h = d; h < p.Hq; h += D) p.lse[size_t(s) * p.Hq + h] = neg_inf;
+    }
+  }
+  const int4 cut = p.ws_cut[blockIdx.x];
+  if (cut.x < 0) return;
+  const int first = int(blockIdx.x) / p.team, lane = int(blockIdx.x) % p.team;
+  const int row = cut.y * p.team + lane, r = blockIdx.y;
+  const int nh = p.part_rows > p.G && r >= p.G ? 1 : 0;
+  const int head = (p.part_rows > p.G ? row * 2 : row) + nh;
+  if (head >= p.Hkv) return;
+  const int n = cut.z - first + 1;         // parts: at most one per team
+  auto part_row = [&](int i) {
+    const int cta = (first + i) * p.team + lane;
+    return size_t(cta * 2 + (i == 0 ? cut.w : 0)) * p.part_rows + r;
+  };
+  // thread i holds the log2-sum-exp of parts i, i + D, ...: all of them in flight at once
+  float mine[(kQ8MaxCtas + D - 1) / D];
+  float m = neg_inf;
+#pragma unroll
+  for (int k = 0; k < (kQ8MaxCtas + D - 1) / D; ++k) {
+    mine[k] = k * D + d < n ? p.ws_lse[part_row(k * D + d)] : neg_inf;
+    m = max_nan(m, mine[k]);
+  }
+  m = warp_max_nan(m);
+  if ((d & 31) == 0) warp_max[d >> 5] = m;
+  __syncthreads();
+#pragma unroll
+  for (int k = 0; k < D / 32; ++k) m = max_nan(m, warp_max[k]);
+  const float off = m == neg_inf ? 0.f : m;
+#pragma unroll
+  for (int k = 0; k < (kQ8MaxCtas + D - 1) / D; ++k)
+    if (k * D + d < n) weight[k * D + d] = fast_exp2(mine[k] - off);
+  __syncthreads();
+  float sum = 0.f, acc = 0.f;
+  const float* src = p.ws_o + part_row(0) * D + d;
+  const size_t step = size_t(p.team) * 2 * p.part_rows * D;       // parts 1, 2, ...: slot 0 of the next teams
+  const float* rest = p.ws_o + (part_row(0) - size_t(cut.w) * p.part_rows) * D + d;
+  for (int i0 = 0; i0 < n; i0 += 8) {
+    float v[8];
+#pragma unroll
+    for (int k = 0; k < 8; ++k) v[k] = i0 + k < n ? (i0 + k == 0 ? *src : rest[(i0 + k) * step]) : 0.f;
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+      const float wt = i0 + k < n ? weight[i0 + k] : 0.f;
+      sum += wt;
+      acc = fmaf(wt, v[k], acc);
+    }
+  }
+  const size_t at = size_t(cut.x) * p.Hq + size_t(head) * p.G + (r - nh * p.G);
+  p.o[at * D + d] = __float2bfloat16_rn(sum == 0.f ? 0.f : acc / sum);
+  if (p.lse && d == 0) p.lse[at] = sum == 0.f ? neg_inf : (m + __log2f(sum)) * 0.69314718055994531f;
 }
 
 }  // namespace attn

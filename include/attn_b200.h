@@ -382,27 +382,28 @@ int attn_kv_read_q8(const void* k_codes, const void* v_codes, const float* k_sca
                     int num_pages, int* device_status, void* stream);
 
 /*
- * attn_decode_q8_split_tokens -- a good split_tokens for attn_decode_paged_q8 (host
- * arithmetic only): a multiple of 128, at most 1024. 0 for invalid arguments.
- */
-int attn_decode_q8_split_tokens(int num_seqs, int Hkv, int max_pages_per_seq, int page_size);
-
-/*
  * attn_decode_paged_q8 -- attn_decode_paged (dense) over the 8-bit cache. The
  * codes enter the tensor cores as they are; the scales enter the scores and the
  * probabilities, so no widened key or value is rounded. Any Hkv; Hq / Hkv from 1
- * to 16. q, o, lse, split_tokens, the workspace (attn_decode_workspace_bytes with
- * the same sizes), empty sequences and bad pages are those of attn_decode_paged.
+ * to 16. q, o, lse, empty sequences and bad pages are those of attn_decode_paged.
+ * There is no split argument: the batch's tiles of 128 tokens are shared out
+ * evenly over the GPU, whatever the lengths, so where a sequence is cut (and with
+ * it the rounding of its result, not its definition) depends on the lengths of
+ * the whole batch; equal calls give equal bits.
+ *   workspace  device scratch, 16-byte aligned, contents on entry ignored, of at
+ *              least attn_decode_paged_q8_workspace_bytes(Hq, Hkv, D) bytes (a
+ *              few MB; 0 for arguments that the decode refuses)
  * q is split into two 8-bit digits scaled to its largest value: its elements
  * below 2^-14 (E4M3) or 2^-8 (int8) of the row's largest lose their last bits
  * (absolute error at most 2^-22 or 2^-14 of the largest). A query row with a NaN
  * or an infinity gives a NaN output row.
  */
+size_t attn_decode_paged_q8_workspace_bytes(int Hq, int Hkv, int D);
 int attn_decode_paged_q8(const void* q, const void* k_codes, const void* v_codes, const float* k_scales,
                          const float* v_scales, const int32_t* block_table, const int32_t* seq_lens, int format,
                          int num_seqs, int Hq, int Hkv, int D, int page_size, int scale_block,
-                         int max_pages_per_seq, int num_pages, float scale, int split_tokens, void* o, float* lse,
-                         void* workspace, size_t workspace_bytes, int* device_status, void* stream);
+                         int max_pages_per_seq, int num_pages, float scale, void* o, float* lse, void* workspace,
+                         size_t workspace_bytes, int* device_status, void* stream);
 
 /*
  * attn_prefill_paged_q8 -- attn_prefill_paged over the 8-bit cache: the chunk's

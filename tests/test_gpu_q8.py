@@ -186,18 +186,21 @@ def test_read_back_foreign_scales_and_bad_pages(cuda_device):
 LENS = [1, 15, 16, 17, 63, 700, 2049, 0, 130]
 
 
-def check_decode(dev, cache, codes, splits, label, lens):
+def check_decode(dev, cache, codes, label, lens):
     kc, vc, ks, vs = codes
     scale = gen.attn_scale(cache.q.shape[-1])
     o_ref, lse_ref = orc.decode_paged_q8(cache.q, kc, vc, ks, vs, cache.block_table, cache.seq_lens, scale)
     o_ref, lse_ref = empty_rows(o_ref, lse_ref, lens)
     args = to(dev, cache.q, kc, vc, ks, vs, cache.block_table, cache.seq_lens)
-    for split in splits:
-        st = torch.zeros(1, dtype=torch.int32, device=dev)
-        o, lse = ab.decode_paged_q8(*args, scale=scale, split_tokens=split, device_status=st)
-        torch.cuda.synchronize()
-        assert int(st) == 0
-        print(label, split, compare_output(o, o_ref, lse, lse_ref, label=f"{label} split={split}"))
+    st = torch.zeros(1, dtype=torch.int32, device=dev)
+    o, lse = ab.decode_paged_q8(*args, scale=scale, device_status=st)
+    torch.cuda.synchronize()
+    assert int(st) == 0
+    print(label, compare_output(o, o_ref, lse, lse_ref, label=label))
+    for b, L in enumerate(lens):      # alone, the sequence is cut elsewhere
+        one = [args[0][b:b + 1], *args[1:5], args[5][b:b + 1], args[6][b:b + 1]]
+        o, lse = ab.decode_paged_q8(*one, scale=scale)
+        compare_output(o, o_ref[b:b + 1], lse, lse_ref[b:b + 1], label=f"{label} alone {b}")
 
 
 @pytest.mark.parametrize("kind", KINDS)
@@ -214,7 +217,7 @@ def test_decode(cuda_device, kind, Hq, Hkv, D, page, block):
             for t in range(0, L, block):
                 used[cache.block_table[b, t // page], t % page // block] = True
         s[~used] = float("nan")
-    check_decode(cuda_device, cache, codes, (64, 192, 1024, None), f"decode {kind}", LENS)
+    check_decode(cuda_device, cache, codes, f"decode {kind}", LENS)
 
 
 @pytest.mark.parametrize("kind", KINDS)
@@ -223,7 +226,7 @@ def test_decode_full_size(cuda_device, kind):
     c = gen.CONFIGS["paged_gqa_decode"]
     cache = gen.paged_decode_inputs(c["N"], c["Hq"], c["Hkv"], c["D"], c["page_size"], c["len_lo"], c["len_hi"],
                                     seed=c["seed"])
-    check_decode(cuda_device, cache, quantized(cache, 16, kind), (None,), f"decode full {kind}", cache.seq_lens)
+    check_decode(cuda_device, cache, quantized(cache, 16, kind), f"decode full {kind}", cache.seq_lens)
 
 
 @pytest.mark.parametrize("kind", KINDS)
@@ -231,7 +234,7 @@ def test_decode_dominant_key(cuda_device, kind):
     S = 3000
     q, k, v = gen.peaked_prefill_inputs(1, 32, 8, S, 128, seed=6500, amp=12.0, period=S)
     cache = gen.paged_from_contiguous(q[:, S - 1], k, v, page_size=16, seed=6501)
-    check_decode(cuda_device, cache, quantized(cache, 16, kind), (256, 4096), f"dominant {kind}", [S])
+    check_decode(cuda_device, cache, quantized(cache, 16, kind), f"dominant {kind}", [S])
 
 
 @pytest.mark.parametrize("kind", KINDS)
@@ -251,11 +254,10 @@ def test_decode_value_scales_far_apart(cuda_device, kind):
     absv = np.abs(orc.q8_dequant(vc, vs))
     bound, _ = orc.decode_paged(cache.q, orc.q8_dequant(kc, ks), absv, cache.block_table, cache.seq_lens, 32, scale)
     args = to(cuda_device, cache.q, kc, vc, ks, vs, cache.block_table, cache.seq_lens)
-    for split in (64, 1024):
-        o, lse = ab.decode_paged_q8(*args, scale=scale, split_tokens=split)
-        err = np.abs(o.double().cpu().numpy() - o_ref)
-        assert (err <= (2.0 ** -9 + 2.0 ** -16) * bound + 2.0 ** -9 * np.abs(o_ref) * 1.01).all()
-        assert np.abs(lse.double().cpu().numpy() - lse_ref).max() <= 1e-3
+    o, lse = ab.decode_paged_q8(*args, scale=scale)
+    err = np.abs(o.double().cpu().numpy() - o_ref)
+    assert (err <= (2.0 ** -9 + 2.0 ** -16) * bound + 2.0 ** -9 * np.abs(o_ref) * 1.01).all()
+    assert np.abs(lse.double().cpu().numpy() - lse_ref).max() <= 1e-3
 
 
 @pytest.mark.parametrize("kind", KINDS)
@@ -266,7 +268,7 @@ def test_decode_zero_scales_and_foreign_ones(cuda_device, kind):
     kc, vc, ks, vs = quantized(cache, 16, kind)
     ks, vs = torch.rand(ks.shape, generator=g) * 0.02, torch.rand(vs.shape, generator=g) * 0.02
     ks[::3], vs[::2] = 0.0, 0.0
-    check_decode(cuda_device, cache, (kc, vc, ks, vs), (64, None), f"foreign scales {kind}", lens)
+    check_decode(cuda_device, cache, (kc, vc, ks, vs), f"foreign scales {kind}", lens)
 
 
 @pytest.mark.parametrize("kind", KINDS)
@@ -283,8 +285,7 @@ def test_decode_nan_stays_with_its_rows(cuda_device, kind):
     vs[cache.block_table[2, 20].long(), 0, 0] = float("nan")
     q[3, 5, 9] = float("inf")
     q[4, 0, 0] = float("nan")
-    o, lse = ab.decode_paged_q8(*to(cuda_device, q, kc, vc, ks, vs, cache.block_table, cache.seq_lens), scale=scale,
-                                split_tokens=256)
+    o, lse = ab.decode_paged_q8(*to(cuda_device, q, kc, vc, ks, vs, cache.block_table, cache.seq_lens), scale=scale)
     o, lse = o.float().cpu().numpy(), lse.cpu().numpy()
     bad = np.zeros((5, 8), bool)
     bad[0, 4:], bad[2, :4], bad[3, 5], bad[4, 0] = True, True, True, True
@@ -303,8 +304,7 @@ def test_decode_bad_pages_and_lengths(cuda_device):
     sl[1], sl[3] = 500, -3            # beyond the table's 208 slots; negative
     bt[1, 12] = 10 ** 6
     st = torch.zeros(1, dtype=torch.int32, device=cuda_device)
-    o, lse = ab.decode_paged_q8(*to(cuda_device, cache.q, kc, vc, ks, vs, bt, sl), scale=scale, split_tokens=64,
-                                device_status=st)
+    o, lse = ab.decode_paged_q8(*to(cuda_device, cache.q, kc, vc, ks, vs, bt, sl), scale=scale, device_status=st)
     assert int(st) == 4
     k, v = orc.q8_dequant(kc, ks), orc.q8_dequant(vc, vs)
     for b, L in ((0, 100), (1, 208)):
@@ -438,10 +438,10 @@ def test_two_streams_at_once(cuda_device):
     lens = [2000, 1500, 900, 40]
     cache = gen.paged_decode_inputs(4, 16, 4, 128, 16, 0, 0, seed=6810, lens=lens, poison=False)
     args = to(cuda_device, cache.q, *quantized(cache, 16, "int8"), cache.block_table, cache.seq_lens)
-    want, wl = ab.decode_paged_q8(*args, split_tokens=128)
+    want, wl = ab.decode_paged_q8(*args)
     streams = [torch.cuda.Stream(device=cuda_device) for _ in range(3)]
     torch.cuda.synchronize()
-    outs = [[ab.decode_paged_q8(*args, split_tokens=128, stream=s) for s in streams] for _ in range(5)]
+    outs = [[ab.decode_paged_q8(*args, stream=s) for s in streams] for _ in range(5)]
     torch.cuda.synchronize()
     for row in outs:
         for o, lse in row:
@@ -457,7 +457,7 @@ def test_binding_refusals(cuda_device):
     for bad in (dict(v_codes=vc.view(torch.int8)), dict(v_scales=vs[:, :1].contiguous()), dict(k_scales=ks.double()),
                 dict(seq_lens=sl[:1]), dict(q=q[:1]), dict(q=q.float()), dict(q=q.transpose(0, 1)),
                 dict(k_codes=kc[:, ::2]), dict(block_table=bt.cpu()), dict(out=torch.empty_like(q)[:, :2]),
-                dict(lse=torch.empty(2, 5, device=cuda_device)), dict(split_tokens=100),
+                dict(lse=torch.empty(2, 5, device=cuda_device)),
                 dict(workspace=torch.empty(16, dtype=torch.uint8, device=cuda_device)),
                 dict(device_status=torch.zeros(1, device=cuda_device))):
         with pytest.raises(ab.AttnError):

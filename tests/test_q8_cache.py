@@ -152,10 +152,10 @@ def _read(lib, **kw):
 
 
 def _decode(lib, **kw):
-    a = _pool(q=FAKE, o=FAKE, lse=None, Hq=9, split=128) | kw
+    a = _pool(q=FAKE, o=FAKE, lse=None, Hq=9) | kw
     return lib.attn_decode_paged_q8(a["q"], a["kc"], a["vc"], a["ks"], a["vs"], a["bt"], a["sl"], a["fmt"], a["N"],
                                     a["Hq"], a["Hkv"], a["D"], a["ps"], a["sb"], a["mp"], a["P"], a["scale"],
-                                    a["split"], a["o"], a["lse"], a["ws"], a["wsb"], None, None)
+                                    a["o"], a["lse"], a["ws"], a["wsb"], None, None)
 
 
 def _prefill(lib, **kw):
@@ -198,9 +198,8 @@ def test_read_refusals(lib, bad):
 
 
 @pytest.mark.parametrize("bad", [dict(q=None), dict(o=None), dict(ws=None), dict(q=at(8)), dict(ws=at(4)),
-                                 dict(lse=at(2)), dict(Hq=0), dict(Hq=8), dict(split=96), dict(split=0),
-                                 dict(scale=0.0), dict(scale=float("nan")), dict(wsb=256),
-                                 dict(N=2 ** 20, Hq=3 * 2 ** 12, Hkv=2 ** 10 * 3)])
+                                 dict(lse=at(2)), dict(Hq=0), dict(Hq=8), dict(scale=0.0),
+                                 dict(scale=float("nan")), dict(wsb=256)])
 def test_decode_refusals(lib, bad):
     assert _decode(lib, **bad) == INVALID
 
@@ -236,14 +235,17 @@ def test_prefill_workspace_bytes(lib):
         assert lib.attn_prefill_paged_q8_workspace_bytes(*bad) == 0
 
 
-@pytest.mark.parametrize("n,hkv,mp,ps", [(1, 1, 1, 16), (1, 8, 2048, 16), (64, 8, 512, 16), (27, 12, 94, 32),
-                                         (500, 1, 3, 256), (1, 1, 2 ** 16, 256)])
-def test_split_tokens(lib, n, hkv, mp, ps):
-    s = ab.binding.decode_q8_split_tokens(n, hkv, mp, ps)
-    assert s % 64 == 0 and 64 <= s <= 4096
-    assert ab.decode_workspace_bytes(n, 4 * hkv, 128, mp, ps, s) > 0
-    assert lib.attn_decode_q8_split_tokens(0, hkv, mp, ps) == 0
-    assert lib.attn_decode_q8_split_tokens(n, hkv, mp, 24) == 0
+def test_decode_workspace_bytes(lib):
+    # {cut sequence} of 16 bytes for each of 320 CTAs; a log2-sum-exp and fp32 O for each of their two parts and
+    # its query rows (those of two heads where D = 64 and a group has at most 8), parts padded to 256 bytes
+    up = lambda x: -(-x // 256) * 256
+    for hq, hkv, d, rows in [(32, 8, 128, 4), (1, 1, 128, 1), (48, 3, 128, 16), (12, 12, 64, 2), (64, 8, 64, 16),
+                             (9, 1, 64, 9)]:
+        want = up(up(320 * 16) + 640 * rows * 4) + 640 * rows * d * 4
+        assert lib.attn_decode_paged_q8_workspace_bytes(hq, hkv, d) == want
+        assert binding.decode_paged_q8_workspace_bytes(hq, hkv, d) == want
+    for bad in [(0, 1, 128), (4, 0, 128), (9, 2, 128), (4, 2, 96), (34, 2, 128)]:
+        assert lib.attn_decode_paged_q8_workspace_bytes(*bad) == 0
 
 
 # ------------------------------------------------------------------ refusals of the binding (CPU tensors)
