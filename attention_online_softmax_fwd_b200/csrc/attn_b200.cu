@@ -645,8 +645,7 @@ bool decode_q8_layout(int Hq, int Hkv, int D, DecodeQ8Layout* L) {
 template <int D, bool I8>
 int launch_append_q8(const KvAppendQ8Params& p, int block, int sms, cudaStream_t stream) {
   const int per_cta = 8 / p.warps_per_unit;
-  const long long units = (long long)p.N * p.blocks * 2 * p.Hkv;
-  long long ctas = (units + per_cta - 1) / per_cta;
+  long long ctas = ((long long)p.units + per_cta - 1) / per_cta;
   if (ctas > (long long)sms * 16) ctas = (long long)sms * 16;
   if (block == 256)
     kv_append_q8_kernel<D, I8, 2><<<dim3(unsigned(ctas)), dim3(256), 0, stream>>>(p);
@@ -656,10 +655,13 @@ int launch_append_q8(const KvAppendQ8Params& p, int block, int sms, cudaStream_t
 }
 
 int launch_read_q8(int format, int D, KvReadQ8Params& p, int sms, cudaStream_t stream) {
-  // about eight CTAs of eight rows per SM over all sequences, at least one for each
-  long long per = ((long long)sms * 8 + p.N - 1) / p.N;
-  const long long rows = ((long long)p.T + 7) / 8;
-  if (per > rows) per = rows;
+  // lanes of a row; about 32 CTAs per SM over all sequences, at least one for each
+  const int vecs = p.Hkv * D / 8;
+  p.group_shift = vecs >= 32 ? 5 : log2_of(vecs);
+  const long long rows = 256 >> p.group_shift;
+  long long per = ((long long)sms * 32 + p.N - 1) / p.N;
+  const long long tiles = ((long long)p.T + rows - 1) / rows;
+  if (per > tiles) per = tiles;
   p.ctas_per_seq = int(per);
   const dim3 grid(unsigned((long long)p.N * per)), cta(256);
   if (format == ATTN_KV_INT8) {
@@ -1110,6 +1112,9 @@ int attn_kv_append_q8(const void* k_new, const void* v_new, void* k_codes, void*
   p.block_shift = log2_of(scale_block);
   p.blocks = int(((long long)T + 2ll * scale_block - 2) / scale_block);
   p.warps_per_unit = scale_block / 16 < 8 ? scale_block / 16 : 8;
+  // far beyond what the device can hold: a unit has at least 64 values
+  if ((long long)num_seqs * p.blocks > 0x3fffffffll / Hkv) return ATTN_ERR_UNSUPPORTED;
+  p.units = unsigned(num_seqs) * unsigned(p.blocks) * 2u * unsigned(Hkv);
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   if (format == ATTN_KV_INT8)
     return D == 128 ? launch_append_q8<128, true>(p, scale_block, sms, s)

@@ -92,6 +92,7 @@ def test_append_zeros_extremes_and_not_finite(cuda_device, kind):
     kc, ks = random_pool(g, 4, 32, 16, 2, 64, kind)
     x = torch.zeros(1, 64, 2, 64, dtype=torch.bfloat16)
     x[0, 16:32] = 3.3e38
+    x[0, 20:24] = -3.3895e38      # the largest bf16
     x[0, 32:48] = 1e-38
     x[0, 50, 0, 3] = float("nan")
     x[0, 51, 1, 7] = -float("inf")
