@@ -1197,6 +1197,9 @@ int attn_decode_paged_q8(const void* q, const void* k_codes, const void* v_codes
   p.rows128 = D == 128 || p.solo ? Hkv : (Hkv + 1) / 2;
   p.team = q8_team(p.rows128);
   p.groups = (p.rows128 + p.team - 1) / p.team;
+  // the kernel counts the batch's tiles in 32 bits (2^30 of them are 140 thousand million tokens)
+  const long long tiles = ((long long)max_pages_per_seq * page_size + kQ8Tok - 1) / kQ8Tok;
+  if (tiles > (1ll << 30) / p.groups / num_seqs) return ATTN_ERR_UNSUPPORTED;
   p.part_rows = L.part_rows;
   p.scale_log2 = scale * 1.4426950408889634f;
 

@@ -129,6 +129,24 @@ struct DecodeQ8Smem {
   static_assert(kR <= 16, "digit rows");
 };
 
+// mbar_wait with its limit counted in clock cycles (4e9, at least two seconds): reading %globaltimer takes
+// long enough to show in every wait of a tile that does not succeed at once.
+__device__ __forceinline__ bool q8_wait(uint64_t* bar, uint32_t parity, volatile int* abort_flag, int* user_status) {
+  if (mbar_try_wait(bar, parity)) return true;
+  const long long t0 = clock64();
+  for (uint32_t i = 1;; ++i) {
+    if (mbar_try_wait(bar, parity)) return true;
+    if ((i & 31u) == 0) {
+      if (*abort_flag) return false;
+      if (clock64() - t0 > 4000000000ll) {
+        *abort_flag = 1;
+        raise_status(user_status, ATTN_ERR_TIMEOUT);
+        return false;
+      }
+    }
+  }
+}
+
 __device__ __forceinline__ void tma_load_3d(void* dst, const CUtensorMap* map, uint64_t* bar, int c0, int c1, int c2) {
   asm volatile(
       "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
@@ -293,39 +311,45 @@ __global__ void __launch_bounds__(kQ8Threads, DecodeQ8Smem<D, NH, GP, I8>::kBloc
   const int lane = threadIdx.x & 31;
   const int capacity = p.max_pages * p.page_size;
 
-  if (threadIdx.x == 0) {
-    abort_word = 0;
-    for (int s = 0; s < NS; ++s) {
-      mbar_init(&full[s], 33);    // the producer's expect_tx arrival and its 32 lanes' scale copies
-      mbar_init(&empty[s], 2);    // the stage's P V products, and the V warp (which a stage without copies needs)
-      mbar_init(&v_go[s], 1);
-    }
-    for (int i = 0; i < 2; ++i) {
+  // tiles of each scan entry's share of the sequences, summed by four threads, the loads first. (A sum fits
+  // an int: sequences of 2^30 tokens would need block tables of terabytes first.)
+  const int per_entry = (p.num_seqs + kQ8Scan - 1) / kQ8Scan;
+  const int scan_at = (threadIdx.x >> 2) * per_entry + (threadIdx.x & 3);
+  const int scan_end = min((int(threadIdx.x >> 2) + 1) * per_entry, p.num_seqs);
+  int first_len = scan_at < scan_end ? __ldg(&p.seq_lens[scan_at]) : 0;
+  // the first 32 lengths, which the K warp walks if its work starts there
+  const int window0 = warp == kQ8KWarp && lane < p.num_seqs ? __ldg(&p.seq_lens[lane]) : 0;
+
+  if (warp == kQ8PvWarp) {
+    if (lane == 0) abort_word = 0;
+    if (lane < NS) {
+      mbar_init(&full[lane], 33);    // the producer's expect_tx arrival and its 32 lanes' scale copies
+      mbar_init(&empty[lane], 2);    // the stage's P V products, and the V warp (which a stage without copies needs)
+      mbar_init(&v_go[lane], 1);
+    } else if (lane < NS + 2) {
+      const int i = lane - NS;
       mbar_init(&s_full[i], 1);
       mbar_init(&s_free[i], kQ8SoftmaxWarps);
       mbar_init(&p_ready[i], kQ8SoftmaxWarps);
       mbar_init(&o_full[i], 1);
       mbar_init(&q_ready[i], 1);
+      mbar_init(&done[i], 1);
+      if (i == 0) mbar_init(ml_ready, kQ8SoftmaxWarps);
     }
-    mbar_init(ml_ready, kQ8SoftmaxWarps);
-    mbar_init(&done[0], 1);
-    mbar_init(&done[1], 1);
     fence_mbar_init();
+  } else if (warp < kQ8SoftmaxWarps) {
+    // digit rows that no query head uses stay zero (q and P digits follow one another)
+    for (int i = threadIdx.x * 16; i < 2 * (L::kQTile + L::kPTile); i += kQ8SoftmaxWarps * 32 * 16)
+      *reinterpret_cast<uint4*>(smem + L::kQT + i) = make_uint4(0, 0, 0, 0);
+    fence_proxy_async_smem();
+  } else if (lane == 0) {
+    if (warp == kQ8KWarp) tma_prefetch_desc(&tm_k);
+    if (warp == kQ8VWarp) tma_prefetch_desc(&tm_v);
   }
-  // digit rows that no query head uses stay zero
-  for (int i = threadIdx.x * 16; i < 2 * L::kQTile; i += kQ8Threads * 16)
-    *reinterpret_cast<uint4*>(smem + L::kQT + i) = make_uint4(0, 0, 0, 0);
-  for (int i = threadIdx.x * 16; i < 2 * L::kPTile; i += kQ8Threads * 16)
-    *reinterpret_cast<uint4*>(smem + L::kPT + i) = make_uint4(0, 0, 0, 0);
-  fence_proxy_async_smem();
-  // tiles of each scan entry's share of the sequences, summed by four threads. (A sum fits an int: sequences of
-  // 2^30 tokens would need block tables of terabytes first.)
-  const int per_entry = (p.num_seqs + kQ8Scan - 1) / kQ8Scan;
   {
     int sum = 0;
-    const int s0 = (threadIdx.x >> 2) * per_entry;
-    for (int i = threadIdx.x & 3; i < per_entry && s0 + i < p.num_seqs; i += 4) {
-      const int len = __ldg(&p.seq_lens[s0 + i]);
+    for (int i = scan_at; i < scan_end; i += 4) {
+      const int len = i == scan_at ? first_len : __ldg(&p.seq_lens[i]);
       if (blockIdx.x == 0 && (len < 0 || len > capacity)) raise_status(p.status, ATTN_ERR_DEVICE_BOUNDS);
       sum += q8_tiles(q8_clamp_len(len, capacity));
     }
@@ -346,7 +370,6 @@ __global__ void __launch_bounds__(kQ8Threads, DecodeQ8Smem<D, NH, GP, I8>::kBloc
 
   if (warp == kQ8KWarp) {
     // ------------------------------------------------------------ producer warp: work, K, scales
-    if (lane == 0) tma_prefetch_desc(&tm_k);
     const int c = lane & 7;            // lane: chunk c of the tile; bit 3: V scales; bit 4: second head of the row
     const bool box_lane = lane < 8 && (c & (p.box / kQ8Chunk - 1)) == 0;   // lane of a copy's first chunk
     const float* sc_src = (lane & 8) ? p.v_scales : p.k_scales;
@@ -354,22 +377,26 @@ __global__ void __launch_bounds__(kQ8Threads, DecodeQ8Smem<D, NH, GP, I8>::kBloc
     const int team = int(blockIdx.x) / p.team;
     const int team_lane = int(blockIdx.x) % p.team;
 
-    // ---- this team's run of the batch's tiles, and the sequence where it starts
-    const long long mine = (long long)scan[2 * lane] + scan[2 * lane + 1];
-    long long incl = mine;
+    // ---- this team's run of the batch's tiles, and the sequence where it starts. (A CTA runs this code once,
+    // at the speed of its instruction fetches: it is kept short, and in 32 bits; the host bounds the tiles.)
+    const int mine = scan[2 * lane] + scan[2 * lane + 1];
+    int incl = mine;
 #pragma unroll
     for (int d = 1; d < 32; d <<= 1) {
-      const long long up = __shfl_up_sync(0xffffffffu, incl, d);
+      const int up = __shfl_up_sync(0xffffffffu, incl, d);
       if (lane >= d) incl += up;
     }
-    const long long per_group = __shfl_sync(0xffffffffu, incl, 31);
-    const long long total = per_group * p.groups;
+    const int per_group = __shfl_sync(0xffffffffu, incl, 31);
+    const int total = per_group * p.groups;
     // at least two tiles for each team (so no team without one between two parts): a cut costs as much as a tile
-    const int teams = int(min((total + 1) / 2, (long long)p.teams));
-    long long pos = team < teams ? total * team / teams : 0;
-    const long long begin = pos, end = team < teams ? total * (team + 1) / teams : 0;
+    const int teams = min((total + 1) / 2, p.teams);
+    const int quot = teams > 0 ? total / teams : 0, extra = total - quot * teams;   // the first `extra` have one more
+    const bool work = team < teams;
+    const int begin = work ? team * quot + min(team, extra) : 0;
+    const int end = work ? begin + quot + (team < extra ? 1 : 0) : 0;
+    int pos = begin;
     int grp = 0, seq = 0, a = 0;       // next tile: tile a of (group, sequence)
-    int win = -1, win_len = 0;         // lengths of sequences 32 win .. 32 win + 31, one per lane
+    int win = 0, win_len = q8_clamp_len(window0, capacity);   // lengths of sequences 32 win .., one per lane
     auto len_at = [&](int s) -> int {
       if ((s >> 5) != win) {
         win = s >> 5;
@@ -378,124 +405,130 @@ __global__ void __launch_bounds__(kQ8Threads, DecodeQ8Smem<D, NH, GP, I8>::kBloc
       }
       return __shfl_sync(0xffffffffu, win_len, s & 31);
     };
-    if (begin < end) {
-      grp = int(begin / per_group);
-      long long x = begin - grp * per_group;
-      const uint32_t at = __ballot_sync(0xffffffffu, incl > x);   // not empty: x < per_group
-      const int l0 = __ffs(int(at)) - 1;
+    if (work) {
+      int x = begin;
+      if (p.groups > 1) {
+        grp = x / per_group;
+        x -= grp * per_group;
+      }
+      const int l0 = __ffs(int(__ballot_sync(0xffffffffu, incl > x))) - 1;   // some lane: x < per_group
       x -= __shfl_sync(0xffffffffu, incl - mine, l0);
       int t = 2 * l0;
       if (x >= scan[t]) x -= scan[t++];
       seq = t * per_entry;
-      for (;; ++seq) {
-        const int tiles = q8_tiles(len_at(seq));
-        if (x < tiles) break;
-        x -= tiles;
-      }
-      a = int(x);
+      for (int tiles; x >= (tiles = q8_tiles(len_at(seq))); ++seq) x -= tiles;
+      a = x;
     }
-    // the next part (a run of tiles of one sequence) is taken one part ahead, its first pages requested
-    struct Part { int seq, grp, a, n, len, tiles; long long pos; };
-    Part nx{};
-    int nx_page = -1;
     auto page_of = [&](int s, int t0) -> int {   // physical page of chunk c of the tile at t0
       const int e = (t0 + c * kQ8Chunk) >> p.page_shift;
       return e < p.max_pages ? __ldg(&p.block_table[size_t(s) * p.max_pages + e]) : -1;
     };
-    auto next_part = [&]() {
-      nx.n = 0;
-      if (pos >= end) return;
-      int len, tiles;
-      for (;;) {
-        if (seq == p.num_seqs) { seq = 0; ++grp; }
-        len = len_at(seq);
-        tiles = q8_tiles(len);
-        if (tiles > a) break;
-        ++seq;
-        a = 0;
-      }
-      const long long left = end - pos;
-      nx.seq = seq; nx.grp = grp; nx.a = a; nx.len = len; nx.tiles = tiles; nx.pos = pos;
-      nx.n = tiles - a < left ? tiles - a : int(left);
-      nx_page = page_of(seq, a * kQ8Tok);
-      pos += nx.n;
-      a += nx.n;
-      if (a == tiles) { a = 0; ++seq; }
-    };
-    next_part();
+    // the part at hand (a run of tiles of one sequence) and the next one, taken while the first tile of this
+    // one is on its way, its first pages requested
+    struct Part { int seq, grp, t_begin, t_end, n, tiles, pos; };
+    Part nx{}, w{};
+    int nx_page = -1, page = -1;
+    int row = 0, part = 0, head0 = 0, head = 0, byte = 0, q_rows = 0;
+    bool head_ok = false;
+    int t0 = 0;
     int4 cut = make_int4(-1, 0, 0, 0);
     int slot = 0;
     uint32_t phase = 0;
     uint32_t pending = 0, pending_phase = 0;
-    bool ok = true;
-    while (ok && nx.n > 0) {
-      const Part w = nx;
-      int page = nx_page;
-      next_part();
-      const int row = w.grp * p.team + team_lane;      // 128-byte row of the tokens
-      if (row >= p.rows128) continue;                  // a lane past the last row
-      const bool whole = w.n == w.tiles;
-      const int part = whole ? -1 : int(blockIdx.x) * 2 + (w.pos == begin ? 0 : 1);
-      if (!whole && w.a == 0) {   // the first part of a cut sequence: this CTA's last work
-        const long long last = w.pos + w.tiles - 1;    // the team of its last tile
-        cut = make_int4(w.seq, w.grp, int(((last + 1) * teams - 1) / total), part & 1);
-      }
-      const int head0 = NH == 2 ? row * 2 : row;       // first KV head of the row's query rows
-      const int head = head0 + (NH == 2 ? lane >> 4 : 0);
-      const bool head_ok = head < p.Hkv && (NH == 2 || lane < 16);
-      const int byte = (p.solo ? row >> 1 : row) * kQ8Row;
-      const int q_rows = min(NH * p.G, p.Hq - head0 * p.G);
-      const int t_begin = w.a * kQ8Tok, t_end = min((w.a + w.n) * kQ8Tok, w.len);
-      for (int t0 = t_begin; t0 < t_end && ok; t0 += kQ8Tok) {
-        const int page_next = t0 + kQ8Tok < t_end ? page_of(w.seq, t0 + kQ8Tok) : -1;
-        const int ntok = min(kQ8Tok, t_end - t0);
-        const bool in_range = page >= 0 && page < p.num_pages;
-        const bool held = c * kQ8Chunk < ntok;
-        const bool good = held && in_range;
-        const uint32_t good_mask = __ballot_sync(0xffffffffu, good) & 0xFFu;
-        const uint32_t box_mask = __ballot_sync(0xffffffffu, good && box_lane);   // copies to issue
-        if (__any_sync(0xffffffffu, held && !in_range) && lane == 0) raise_status(p.status, ATTN_ERR_DEVICE_BOUNDS);
-        const int in_page = (t0 + c * kQ8Chunk) & (p.page_size - 1);
-        const bool copy_scale = good && head_ok;
-        const float* sc = sc_src + (copy_scale ? (size_t(page) * blocks_per_page + (in_page >> p.block_shift)) * p.Hkv + head
-                                               : size_t(0));
-        const bool first = t0 == t_begin;
-        uint8_t* stage = smem + slot * L::kStageBytes;
-        int* job = reinterpret_cast<int*>(smem + L::kJob) + slot * 12;
-        if (!__all_sync(0xffffffffu, mbar_wait(&empty[slot], phase ^ 1u, abort_flag, p.status))) { ok = false; break; }
-        if (lane < 8) job[lane] = page;
-        if (lane == 0) {
-          job[8] = t0;
-          job[9] = byte;
-          job[10] = int(box_mask);
-          TileInfo ti;
-          ti.seq = w.seq; ti.split = part; ti.kvh = row; ti.t0 = t0;
-          ti.ntok = ntok;
-          ti.bad = int(~good_mask & 0xFFu);
-          ti.flags = (first ? 1 : 0) | (t0 + kQ8Tok >= t_end ? 2 : 0);
-          ti.len = w.len;
-          info[slot] = ti;
-          const uint32_t qbytes = first ? uint32_t(q_rows * D * 2) : 0u;
-          mbar_arrive_expect_tx(&full[slot], uint32_t(__popc(box_mask)) * uint32_t(2 * kQ8Row * p.box) + qbytes);
-          if (first)
-            bulk_load(smem + L::kQRows + slot * L::kQBytes, p.q + (size_t(w.seq) * p.Hq + size_t(head0) * p.G) * D, qbytes,
-                      &full[slot]);
+    bool ok = true, fetch = true;
+    for (;;) {
+      if (fetch) {
+        fetch = false;
+        nx.n = 0;
+        if (pos < end) {
+          int len, tiles;
+          for (;;) {
+            if (seq == p.num_seqs) { seq = 0; ++grp; }
+            len = len_at(seq);
+            tiles = q8_tiles(len);
+            if (tiles > a) break;
+            ++seq;
+            a = 0;
+          }
+          nx.seq = seq; nx.grp = grp; nx.tiles = tiles; nx.pos = pos;
+          nx.n = min(tiles - a, end - pos);
+          nx.t_begin = a * kQ8Tok;
+          nx.t_end = min((a + nx.n) * kQ8Tok, len);
+          nx_page = page_of(seq, nx.t_begin);
+          pos += nx.n;
+          a += nx.n;
+          if (a == tiles) { a = 0; ++seq; }
         }
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&v_go[slot]);
-        if ((box_mask >> lane) & 1)
-          tma_load_3d(stage + c * (kQ8Chunk * kQ8Row), &tm_k, &full[slot], byte, in_page, page);
-        if (copy_scale) cp_async4(scales + slot * 16 * NH + lane, sc);
-        cp_async_arrive_noinc(&full[slot]);
-        __syncwarp();
-        pending |= 1u << slot;
-        pending_phase = (pending_phase & ~(1u << slot)) | (phase << slot);
-        if (++slot == NS) { slot = 0; phase ^= 1u; }
-        page = page_next;
       }
+      if (t0 >= w.t_end) {   // the next part
+        if (nx.n == 0) break;
+        w = nx;
+        t0 = w.t_begin;
+        page = nx_page;
+        row = w.grp * p.team + team_lane;                // 128-byte row of the tokens
+        if (row >= p.rows128) break;                     // a lane past the last row: in the last group only
+        const bool whole = w.n == w.tiles;
+        part = whole ? -1 : int(blockIdx.x) * 2 + (w.pos == begin ? 0 : 1);
+        if (!whole && w.t_begin == 0) {   // the first part of a cut sequence, this CTA's last work
+          const int last = w.pos + w.tiles - 1, wide = extra * (quot + 1);   // its last tile, and that one's team
+          cut = make_int4(w.seq, w.grp, last < wide ? last / (quot + 1) : extra + (last - wide) / quot, part & 1);
+        }
+        head0 = NH == 2 ? row * 2 : row;                 // first KV head of the row's query rows
+        head = head0 + (NH == 2 ? lane >> 4 : 0);
+        head_ok = head < p.Hkv && (NH == 2 || lane < 16);
+        byte = (p.solo ? row >> 1 : row) * kQ8Row;
+        q_rows = min(NH * p.G, p.Hq - head0 * p.G);
+      }
+      const int page_next = t0 + kQ8Tok < w.t_end ? page_of(w.seq, t0 + kQ8Tok) : -1;
+      const int ntok = min(kQ8Tok, w.t_end - t0);
+      const bool in_range = page >= 0 && page < p.num_pages;
+      const bool held = c * kQ8Chunk < ntok;
+      const bool good = held && in_range;
+      const uint32_t good_mask = __ballot_sync(0xffffffffu, good) & 0xFFu;
+      const uint32_t box_mask = __ballot_sync(0xffffffffu, good && box_lane);   // copies to issue
+      if (__any_sync(0xffffffffu, held && !in_range) && lane == 0) raise_status(p.status, ATTN_ERR_DEVICE_BOUNDS);
+      const int in_page = (t0 + c * kQ8Chunk) & (p.page_size - 1);
+      const bool copy_scale = good && head_ok;
+      const float* sc = sc_src + (copy_scale ? (size_t(page) * blocks_per_page + (in_page >> p.block_shift)) * p.Hkv + head
+                                             : size_t(0));
+      const bool first = t0 == w.t_begin;
+      int* job = reinterpret_cast<int*>(smem + L::kJob) + slot * 12;
+      ok = __all_sync(0xffffffffu, q8_wait(&empty[slot], phase ^ 1u, abort_flag, p.status));
+      if (!ok) break;
+      if (lane < 8) job[lane] = page;
+      if (lane == 0) {
+        job[8] = t0;
+        job[9] = byte;
+        job[10] = int(box_mask);
+        TileInfo ti;
+        ti.seq = w.seq; ti.split = part; ti.kvh = row; ti.t0 = t0;
+        ti.ntok = ntok;
+        ti.bad = int(~good_mask & 0xFFu);
+        ti.flags = (first ? 1 : 0) | (t0 + kQ8Tok >= w.t_end ? 2 : 0);
+        ti.len = 0;
+        info[slot] = ti;
+        const uint32_t qbytes = first ? uint32_t(q_rows * D * 2) : 0u;
+        mbar_arrive_expect_tx(&full[slot], uint32_t(__popc(box_mask)) * uint32_t(2 * kQ8Row * p.box) + qbytes);
+        if (first)
+          bulk_load(smem + L::kQRows + slot * L::kQBytes, p.q + (size_t(w.seq) * p.Hq + size_t(head0) * p.G) * D, qbytes,
+                    &full[slot]);
+      }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&v_go[slot]);
+      if ((box_mask >> lane) & 1)
+        tma_load_3d(smem + slot * L::kStageBytes + c * (kQ8Chunk * kQ8Row), &tm_k, &full[slot], byte, in_page, page);
+      if (copy_scale) cp_async4(scales + slot * 16 * NH + lane, sc);
+      cp_async_arrive_noinc(&full[slot]);
+      __syncwarp();
+      pending |= 1u << slot;
+      pending_phase = (pending_phase & ~(1u << slot)) | (phase << slot);
+      if (++slot == NS) { slot = 0; phase ^= 1u; }
+      page = page_next;
+      t0 += kQ8Tok;
+      fetch = first;
     }
     if (lane == 0) p.ws_cut[blockIdx.x] = cut;
-    if (ok && __all_sync(0xffffffffu, mbar_wait(&empty[slot], phase ^ 1u, abort_flag, p.status))) {
+    if (ok && __all_sync(0xffffffffu, q8_wait(&empty[slot], phase ^ 1u, abort_flag, p.status))) {
       if (lane == 0) {   // end-of-work marker: a stage with no copies
         TileInfo ti{};
         ti.flags = 4;
@@ -516,10 +549,9 @@ __global__ void __launch_bounds__(kQ8Threads, DecodeQ8Smem<D, NH, GP, I8>::kBloc
     }
   } else if (warp == kQ8VWarp) {
     // ------------------------------------------------------------ producer warp: V, as the first one says
-    if (lane == 0) tma_prefetch_desc(&tm_v);
     int slot = 0;
     uint32_t phase = 0;
-    while (__all_sync(0xffffffffu, mbar_wait(&v_go[slot], phase, abort_flag, p.status))) {
+    while (__all_sync(0xffffffffu, q8_wait(&v_go[slot], phase, abort_flag, p.status))) {
       const int* job = reinterpret_cast<const int*>(smem + L::kJob) + slot * 12;
       const int mask = job[10];
       if (mask < 0) break;   // end of work
@@ -539,10 +571,10 @@ __global__ void __launch_bounds__(kQ8Threads, DecodeQ8Smem<D, NH, GP, I8>::kBloc
     const uint64_t k_desc0 = make_sdesc_rows(smem_u32(smem));
     int slot = 0, sb = 0, qb = 1;
     uint32_t phase = 0, f_ph = 1;   // a fresh s_free lets the first two tiles pass
-    while (__all_sync(0xffffffffu, mbar_wait(&full[slot], phase, abort_flag, p.status))) {
+    while (__all_sync(0xffffffffu, q8_wait(&full[slot], phase, abort_flag, p.status))) {
       const int flags = info[slot].flags, row = info[slot].kvh;
       if (flags & 4) break;
-      if (!__all_sync(0xffffffffu, mbar_wait(&s_free[sb], f_ph, abort_flag, p.status))) break;
+      if (!__all_sync(0xffffffffu, q8_wait(&s_free[sb], f_ph, abort_flag, p.status))) break;
       const int half = D == 64 && NH == 1 ? row & 1 : 0;   // solo: the head's half of the row
       if (flags & 1) {
         // the item's query rows as digits, scaled by a power of two (exact). The buffer's last reader, the
@@ -551,36 +583,55 @@ __global__ void __launch_bounds__(kQ8Threads, DecodeQ8Smem<D, NH, GP, I8>::kBloc
         uint8_t* q_tile = smem + L::kQT + qb * L::kQTile;
         float* qf = reinterpret_cast<float*>(smem + L::kQf) + qb * R;
         const int head0 = NH == 2 ? row * 2 : row;
-        for (int i = 0; i < NH * p.G; ++i) {
+        const int n_rows = NH == 2 && head0 + 1 >= p.Hkv ? p.G : NH * p.G;
+        // eight lanes a row, D / 8 values each, four rows at a time
+        constexpr int E = D / 8;
+        const int part8 = lane & 7;
+        for (int i0 = 0; i0 < n_rows; i0 += 4) {
+          const int i = min(i0 + (lane >> 3), n_rows - 1);   // a repeated last row writes the same again
           const int nh = NH == 2 && i >= p.G ? 1 : 0;
-          if (head0 + nh >= p.Hkv) break;
           const int r = nh * GP + (i - nh * p.G);            // digit row
-          constexpr int E = D / 32;   // values per lane
-          const uint32_t* src =
-              reinterpret_cast<const uint32_t*>(smem + L::kQRows + slot * L::kQBytes + i * D * 2) + lane * (E / 2);
+          const uint4* src = reinterpret_cast<const uint4*>(smem + L::kQRows + slot * L::kQBytes + (i * D + part8 * E) * 2);
           uint32_t w[E / 2];
           uint32_t top = 0;
 #pragma unroll
-          for (int k = 0; k < E / 2; ++k) {
-            w[k] = src[k];
-            top = max(top, max((w[k] << 16) & 0x7FFF0000u, w[k] & 0x7FFF0000u));
+          for (int k = 0; k < E / 8; ++k) {
+            const uint4 v = src[k];
+            w[4 * k] = v.x; w[4 * k + 1] = v.y; w[4 * k + 2] = v.z; w[4 * k + 3] = v.w;
           }
-          top = __reduce_max_sync(0xffffffffu, top);
+#pragma unroll
+          for (int k = 0; k < E / 2; ++k) top = __vmaxu2(top, w[k] & 0x7FFF7FFFu);
+          top = max(top & 0xFFFF0000u, top << 16);
+#pragma unroll
+          for (int d = 1; d < 8; d <<= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, d));
           const int e = int(top >> 23) - 127, mant = int(top >> 16) & 0x7F;
           const bool finite = top < 0x7F800000u;
           // the largest value lands in (224, 448] or [16320, 32639]
           int sh = I8 ? 14 - e - (mant == 0x7F ? 1 : 0) : 8 - e - (mant > 0x60 ? 1 : 0);
           sh = min(sh, 118);
           const float up = finite ? __uint_as_float(uint32_t(sh + 127) << 23) : 0.f;
-          if (lane == 0)
+          if (part8 == 0)
             qf[r] = finite ? p.scale_log2 * __uint_as_float(uint32_t(127 - sh) << 23) : __int_as_float(0x7fc00000);
+          uint32_t hi[E / 4], lo[E / 4];
 #pragma unroll
-          for (int k = 0; k < E / 2; ++k) {
-            uint32_t hi = 0, lo = 0;
-            if (finite) two_digits<I8>(bf16_lo(w[k]) * up, bf16_hi(w[k]) * up, hi, lo);
-            const int byte = (half + nh) * 64 + lane * E + 2 * k;
-            *reinterpret_cast<uint16_t*>(q_tile + row_unit(r, byte >> 4) + (byte & 15)) = uint16_t(hi);
-            *reinterpret_cast<uint16_t*>(q_tile + row_unit(R + r, byte >> 4) + (byte & 15)) = uint16_t(lo);
+          for (int k = 0; k < E / 4; ++k) {
+            uint32_t h0 = 0, l0 = 0, h1 = 0, l1 = 0;
+            if (finite) {
+              two_digits<I8>(bf16_lo(w[2 * k]) * up, bf16_hi(w[2 * k]) * up, h0, l0);
+              two_digits<I8>(bf16_lo(w[2 * k + 1]) * up, bf16_hi(w[2 * k + 1]) * up, h1, l1);
+            }
+            hi[k] = h0 | (h1 << 16);
+            lo[k] = l0 | (l1 << 16);
+          }
+          const int at = (half + nh) * 64 + part8 * E;       // byte of the row
+          uint8_t* hi_at = q_tile + row_unit(r, at >> 4) + (at & 15);
+          uint8_t* lo_at = q_tile + row_unit(R + r, at >> 4) + (at & 15);
+          if constexpr (E == 16) {
+            *reinterpret_cast<uint4*>(hi_at) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+            *reinterpret_cast<uint4*>(lo_at) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+          } else {
+            *reinterpret_cast<uint2*>(hi_at) = make_uint2(hi[0], hi[1]);
+            *reinterpret_cast<uint2*>(lo_at) = make_uint2(lo[0], lo[1]);
           }
         }
         fence_proxy_async_smem();
@@ -619,9 +670,9 @@ __global__ void __launch_bounds__(kQ8Threads, DecodeQ8Smem<D, NH, GP, I8>::kBloc
       const uint64_t v_desc0 = make_sdesc_rows(smem_u32(smem + L::kTileBytes));
       int slot = 0, pb = 0;
       uint32_t phase = 0, p_ph = 0;
-      while (mbar_wait(&full[slot], phase, abort_flag, p.status)) {
+      while (q8_wait(&full[slot], phase, abort_flag, p.status)) {
         if (info[slot].flags & 4) break;
-        if (!mbar_wait(&p_ready[pb], p_ph, abort_flag, p.status)) break;
+        if (!q8_wait(&p_ready[pb], p_ph, abort_flag, p.status)) break;
         tc_fence_after();
         const uint64_t v_desc = v_desc0 + uint64_t(slot * (L::kStageBytes >> 4));
         const uint64_t p_desc = p_desc0 + uint64_t(pb * (L::kPTile >> 4));
@@ -659,7 +710,7 @@ __global__ void __launch_bounds__(kQ8Threads, DecodeQ8Smem<D, NH, GP, I8>::kBloc
 #pragma unroll
     for (int h = 0; h < GP; ++h) o[0][h] = o[1][h] = o[2][h] = o[3][h] = 0.f;
     auto wait = [&](uint64_t* bar, uint32_t ph) -> bool {   // the same answer in the whole warp
-      return __all_sync(0xffffffffu, mbar_wait(bar, ph, abort_flag, p.status));
+      return __all_sync(0xffffffffu, q8_wait(bar, ph, abort_flag, p.status));
     };
     // O^T of tile number t: thread = head dimension, one accumulator per warp's tokens
     auto add_tile = [&](int t) -> bool {
@@ -692,14 +743,18 @@ __global__ void __launch_bounds__(kQ8Threads, DecodeQ8Smem<D, NH, GP, I8>::kBloc
       return true;
     };
 
+    bool drain = false;   // the part's last tile has been weighted; its O^T is still to be added
     while (ok) {
+     bool first = false, last = false;
+     if (!drain) {
       const int sb = tile & 1;
       const uint32_t t_ph = uint32_t(tile >> 1) & 1u;   // this tile's use of its double buffers
       if (!wait(&full[slot], phase)) { ok = false; break; }
       const TileInfo ti = info[slot];
       if (ti.flags & 4) break;
       uint8_t* stage = smem + slot * L::kStageBytes;
-      const bool first = (ti.flags & 1) != 0;
+      first = (ti.flags & 1) != 0;
+      last = (ti.flags & 2) != 0;
       if (first) {
         seq = ti.seq; part = ti.split; row = ti.kvh;
         if (!wait(&q_ready[item_no & 1], uint32_t(item_no >> 1) & 1u)) { ok = false; break; }
@@ -714,7 +769,6 @@ __global__ void __launch_bounds__(kQ8Threads, DecodeQ8Smem<D, NH, GP, I8>::kBloc
         for (int h = 0; h < GP; ++h) o[0][h] = o[1][h] = o[2][h] = o[3][h] = 0.f;
         ++item_no;
       }
-      const bool last = (ti.flags & 2) != 0;
       const bool valid = tok < ti.ntok && !((ti.bad >> (tok >> 4)) & 1);
       if (!valid) {   // a V row that was not copied: 0 * (stale bytes) must not reach O
         uint4* v_row = reinterpret_cast<uint4*>(stage + L::kTileBytes + tok * kQ8Row);
@@ -778,11 +832,15 @@ __global__ void __launch_bounds__(kQ8Threads, DecodeQ8Smem<D, NH, GP, I8>::kBloc
       __syncwarp();
       if (lane == 0) mbar_arrive(&p_ready[sb]);
 
-      if (!first && !add_tile(tile - 1)) { ok = false; break; }
-      if (++slot == NS) { slot = 0; phase ^= 1u; }
-      ++tile;
-      if (!last) continue;
-      if (!add_tile(tile - 1)) { ok = false; break; }
+     }
+      if ((drain || !first) && !add_tile(tile - 1)) { ok = false; break; }
+      if (!drain) {
+        if (++slot == NS) { slot = 0; phase ^= 1u; }
+        ++tile;
+        drain = last;
+        continue;
+      }
+      drain = false;
 
       // ---- the part's result: the four warps' accumulators onto common maxima
 #pragma unroll
@@ -801,34 +859,41 @@ __global__ void __launch_bounds__(kQ8Threads, DecodeQ8Smem<D, NH, GP, I8>::kBloc
       const int head = (NH == 2 ? row * 2 : row) + my_half;   // KV head whose dims this thread may hold
       const int dim = D == 64 ? tok & 63 : tok;
       const bool mine = head < p.Hkv && (D == 128 || NH == 2 || (tok >> 6) == (row & 1));
+      const size_t at0 = part < 0 ? size_t(seq) * p.Hq + size_t(head) * p.G : size_t(part) * p.part_rows + my_half * p.G;
+      // lane 4 h + w: warp w's share of query head h (eight heads at a time)
+      const int w4 = lane & 3;
 #pragma unroll
-      for (int h = 0; h < GP; ++h) {
-        if (h >= p.G || !mine) continue;
-        const float* mh = ml + (my_half * GP + h) * 3;
-        float mx = neg_inf, my = neg_inf;
-#pragma unroll
-        for (int w = 0; w < 4; ++w) {
-          mx = max_nan(mx, mh[w * R * 3]);
-          my = max_nan(my, mh[w * R * 3 + 1]);
-        }
+      for (int h0 = 0; h0 < GP; h0 += 8) {
+        const int h = min(h0 + (lane >> 2), GP - 1);
+        const float* m = ml + (w4 * R + my_half * GP + h) * 3;
+        float mx = m[0], my = m[1];
+        mx = max_nan(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
+        my = max_nan(my, __shfl_xor_sync(0xffffffffu, my, 1));
+        mx = max_nan(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
+        my = max_nan(my, __shfl_xor_sync(0xffffffffu, my, 2));
         const float offx = mx == neg_inf ? 0.f : mx, offy = my == neg_inf ? 0.f : my;
-        float lsum = 0.f, acc = 0.f;
-#pragma unroll
-        for (int w = 0; w < 4; ++w) {
-          lsum = fmaf(mh[w * R * 3 + 2], fast_exp2(mh[w * R * 3] - offx), lsum);
-          acc = fmaf(o[w][h], fast_exp2(mh[w * R * 3 + 1] - offy), acc);
-        }
+        float lsum = m[2] * fast_exp2(m[0] - offx);
+        lsum += __shfl_xor_sync(0xffffffffu, lsum, 1);
+        lsum += __shfl_xor_sync(0xffffffffu, lsum, 2);
         // lsum is 0 only if every page was invalid; a NaN stays a NaN
-        const float out = lsum == 0.f ? 0.f : acc * fast_exp2(offy - offx) * (1.f / kPScale) / lsum;
-        const float lse2 = lsum == 0.f ? neg_inf : mx + __log2f(lsum);
-        if (part < 0) {
-          const size_t at = size_t(seq) * p.Hq + size_t(head) * p.G + h;
-          p.o[at * D + dim] = __float2bfloat16_rn(out);
-          if (p.lse && dim == 0) p.lse[at] = lse2 * 0.69314718055994531f;
-        } else {
-          const size_t at = size_t(part) * p.part_rows + my_half * p.G + h;
-          p.ws_o[at * D + dim] = out;
-          if (dim == 0) p.ws_lse[at] = lse2;
+        const float share = lsum == 0.f ? 0.f : __fdividef(fast_exp2(m[1] - offy) * fast_exp2(offy - offx) * (1.f / kPScale), lsum);
+        if (p.lse || part >= 0) {
+          const float lse2 = lsum == 0.f ? neg_inf : mx + __log2f(lsum);
+          // one warp of each head half writes: lane 4 h
+          if ((warp & (NH == 2 ? 1 : 3)) == 0 && w4 == 0 && h0 + (lane >> 2) < p.G && head < p.Hkv) {
+            if (part < 0) p.lse[at0 + h] = lse2 * 0.69314718055994531f;
+            else p.ws_lse[at0 + h] = lse2;
+          }
+        }
+#pragma unroll
+        for (int k = 0; k < 8 && k < GP; ++k) {
+          float out = 0.f;
+#pragma unroll
+          for (int w = 0; w < 4; ++w) out = fmaf(o[w][h0 + k], __shfl_sync(0xffffffffu, share, 4 * k + w), out);
+          if (h0 + k < p.G && mine) {
+            if (part < 0) p.o[(at0 + h0 + k) * D + dim] = __float2bfloat16_rn(out);
+            else p.ws_o[(at0 + h0 + k) * D + dim] = out;
+          }
         }
       }
     }
