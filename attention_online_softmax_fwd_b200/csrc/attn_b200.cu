@@ -577,7 +577,9 @@ bool valid_q8_block(int block, int page_size) {
 template <int D, int NH, int GP, bool I8>
 int launch_decode_q8(const CUtensorMap& tk, const CUtensorMap& tv, DecodeQ8Params& p, int sms, cudaStream_t stream) {
   using L = DecodeQ8Smem<D, NH, GP, I8>;
-  if (int st = set_smem_once<decode_q8_kernel<D, NH, GP, I8>>(L::kDynamic)) return st;
+  // the kernel moves registers between its warpgroups: the launch allocation must cover the split
+  if (int st = set_smem_once<decode_q8_kernel<D, NH, GP, I8>>(L::kDynamic, (L::kRegPool + kQ8Threads - 1) / kQ8Threads))
+    return st;
   const int ctas = sms * L::kBlocks < kQ8MaxCtas ? sms * L::kBlocks : kQ8MaxCtas;
   p.teams = ctas / p.team;
   const unsigned grid = unsigned(p.teams * p.team);

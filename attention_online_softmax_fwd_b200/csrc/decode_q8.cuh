@@ -9,7 +9,7 @@
 // split into two 8-bit digits so that nothing of it is lost:
 //   S^T = Kc (128 tokens x D) * [q_hi; q_lo]^T,  q * 2^a = q_hi + q_lo / 16 (E4M3)
 //                                                        = 256 q_hi + q_lo  (int8)
-//   O^T_w = Vc^T (128 dims x 32 tokens) * [p_hi; p_lo]^T  for each warp w's 32 tokens
+//   O^T = Vc^T (128 dims x 128 tokens) * [p_hi; p_lo]^T
 // E4M3: a bf16 value has 8 significant bits, a code 4, so two codes hold q exactly
 // down to 2^-14 of the row's largest value; the products accumulate in fp32.
 // int8: q becomes a 16-bit integer (exact down to 2^-8 of the row's largest value)
@@ -33,21 +33,24 @@
 // run is written at once; the parts of one that is cut are merged by
 // decode_q8_merge_kernel, and each CTA has two at most, whatever the lengths.
 //
-// A CTA has four softmax warps (one token per thread of a tile), two producer warps
+// A CTA has two softmax warpgroups (one token of a tile per thread), two producer warps
 // (one walks the lengths and block tables, copies K by TMA and the scales by
 // cp.async, and hands each tile's pages to the other, which copies V: one warp
 // takes about 100 cycles to issue a copy, and 16-token pages need 16 of them a
 // tile, so with one producer the issue took longer than the tile's share of the
 // HBM time, 2570 cycles with two CTAs per SM), a warp that turns the query rows
 // into digits and issues the score products, and one that issues the P V products.
-// Scores run a tile ahead of the softmax, and O of a tile is added to the
-// accumulators while the next tile's P V runs (S^T, P and O^T are double-buffered).
-// Each softmax warp keeps its own running maxima X, Y for its 32 tokens of every
-// tile, and its own accumulator columns, so the warps exchange no maximum: the
-// P V product of a tile is four MMAs of K = 32, one per warp. O stays in fp32
-// registers (thread = head dimension) and is rescaled there by each warp's
-// factor, which is why TMEM holds only the tile's own products. The four
-// accumulators are merged when the CTA's part of the sequence ends.
+// The warpgroups take alternate tiles, each with its own buffers of S^T, P and O^T:
+// a tile's way through scores, softmax, P V and accumulation is some 1500 to 3000
+// cycles of latency, by the number of query rows, so four tiles a SM are under way
+// at a time. The four warps of a warpgroup exchange the tile's maxima of y once, so
+// that its 128 tokens share one reference and P V is one accumulation. (Without the
+// exchange, each warp keeping a reference and accumulators of its own, O took four
+// times the registers and tensor-memory reads: 92 us instead of XX for 16 sequences
+// of 8192 tokens with 8 query heads a group.) O stays in fp32 registers (thread =
+// head dimension) and is rescaled there when Y grows, which is why TMEM holds only
+// the tile's own products. When the CTA's part of the sequence ends, the warpgroup
+// of its last tile adds the other's O, handed over through TMEM.
 #pragma once
 
 #include "decode.cuh"
@@ -58,11 +61,11 @@ constexpr int kQ8Tok = 128;          // tokens per tile
 constexpr int kQ8Row = 128;          // bytes of a tile's row
 constexpr int kQ8Chunk = 16;         // tokens whose page and scales are looked up together
 constexpr int kQ8MaxBox = 64;        // tokens per TMA copy: min(page_size, 64)
-constexpr int kQ8SoftmaxWarps = 4;
-constexpr int kQ8KWarp = kQ8SoftmaxWarps, kQ8VWarp = kQ8KWarp + 1, kQ8ScoreWarp = kQ8KWarp + 2,
+constexpr int kQ8SoftmaxWarps = 4;   // of a warpgroup; warpgroups 0 and 1 are softmax, 2 the helpers
+constexpr int kQ8KWarp = 2 * kQ8SoftmaxWarps, kQ8VWarp = kQ8KWarp + 1, kQ8ScoreWarp = kQ8KWarp + 2,
               kQ8PvWarp = kQ8KWarp + 3;
-constexpr int kQ8Threads = (kQ8SoftmaxWarps + 4) * 32;
-constexpr int kQ8Scan = 64;          // sums of tile counts, one for each four threads' sequences
+constexpr int kQ8Threads = (2 * kQ8SoftmaxWarps + 4) * 32;
+constexpr int kQ8Scan = 64;          // sums of tile counts, each over four threads' sequences
 constexpr int kQ8MaxTeam = 8;        // lanes of a team
 constexpr int kQ8MaxCtas = 320;      // CTAs of a call at most (two on each of 148 SMs); fixes the workspace size
 
@@ -99,32 +102,37 @@ struct DecodeQ8Smem {
   static constexpr int kBlocks = kR <= 8 ? 2 : 1;          // resident CTAs per SM
   static constexpr int kQTile = kN * kQ8Row;               // digit rows of q
   static constexpr int kPTile = kN * kQ8Tok;               // digit rows of P
-  static constexpr int kPerStage = kStageBytes + kQBytes + 64 * NH + 32 + 48 + 24;
-  static constexpr int kFixed = 1024 + 2 * kQTile + 2 * kPTile + 4 * (4 * 4 * kR + 3 * 4 * kR + 2 * kR) + 4 * kQ8Scan +
-                                8 * 13 + 64;
+  static constexpr int kPerStage = kStageBytes + 64 * NH + 32 + 48 + 24;
+  static constexpr int kFixed = 1024 + 2 * kQBytes + 2 * kQTile + 2 * kPTile + 4 * (4 * 4 * kR + 2 * 2 * 4 * kR + 2 * kR + 3 * kR) +
+                                4 * kQ8Scan + 8 * 18 + 64;
   static constexpr int kFit = (233472 / kBlocks - 1024 - kFixed) / kPerStage;
   static constexpr int kStages = kFit < 8 ? kFit : 8;
   static constexpr int kQT = kStages * kStageBytes;                    // q digits [item parity], 1024-byte aligned
   static constexpr int kPT = kQT + 2 * kQTile;                         // P digits [tile parity]
-  static constexpr int kQRows = kPT + 2 * kPTile;                      // query rows per stage
-  static constexpr int kScales = kQRows + kQBytes * kStages;           // [stage][head half][K 8 | V 8] floats
+  static constexpr int kQRows = kPT + 2 * kPTile;                      // query rows [part parity]
+  static constexpr int kScales = kQRows + 2 * kQBytes;                 // [stage][head half][K 8 | V 8] floats
   static constexpr int kInfo = kScales + 64 * NH * kStages;               // TileInfo per stage
   static constexpr int kJob = kInfo + 32 * kStages;                    // V copies of a stage: 8 pages, t0, byte, mask
-  static constexpr int kAlpha = kJob + 48 * kStages;                   // [tile mod 4][warp][kR] floats
-  static constexpr int kMl = kAlpha + 4 * 4 * 4 * kR;                  // [warp][kR] x {X, Y, l} floats
-  static constexpr int kQf = kMl + 4 * 3 * 4 * kR;                     // [item parity][kR] floats
-  static constexpr int kScan = (kQf + 4 * 2 * kR + 7) / 8 * 8;         // sums of tile counts
+  static constexpr int kYmax = (kJob + 48 * kStages + 15) / 16 * 16;   // [warpgroup][use parity][kR][warp] floats
+  static constexpr int kMl = kYmax + 4 * 4 * 4 * kR;                   // [warpgroup][warp][kR] x {X, l} floats
+  static constexpr int kQf = kMl + 4 * 2 * 2 * 4 * kR;                 // [part parity][kR] floats
+  static constexpr int kSwap = kQf + 4 * 2 * kR;                       // [kR] x {X, Y, l} of the other warpgroup
+  static constexpr int kScan = (kSwap + 4 * 3 * kR + 7) / 8 * 8;         // sums of tile counts
   static constexpr int kBars = (kScan + 4 * kQ8Scan + 7) / 8 * 8;      // mbarriers
   // full[kStages], empty[kStages], v_go[kStages], s_full[2], s_free[2], p_ready[2], o_full[2], q_ready[2],
-  // ml_ready, done[2]
-  static constexpr int kTotal = kBars + 8 * (3 * kStages + 13);
+  // ml_ready[2], done[2], y_ready[2], swap_full, swap_free
+  static constexpr int kTotal = kBars + 8 * (3 * kStages + 18);
   static constexpr int kDynamic = kTotal + 1024;
   static constexpr int kSBuf = NH * kN;                    // columns of one score buffer: kN for each head half
-  static constexpr int kTmemUse = 2 * kSBuf + 2 * 4 * kN;
-  static constexpr int kTmemCols = kTmemUse <= 256 ? 256 : 512;
+  static constexpr int kTmemSwap = 2 * kSBuf + 2 * kN;     // O of the warpgroup that does not finish a part
+  static constexpr int kTmemUse = kTmemSwap + GP;
+  // registers of a helper and of a softmax thread; together they are the block's launch allocation
+  static constexpr int kHelperRegs = kBlocks == 1 ? 80 : 64, kSoftmaxRegs = kBlocks == 1 ? 208 : 88;
+  static constexpr int kRegPool = 128 * kHelperRegs + 256 * kSoftmaxRegs;
+  static constexpr int kTmemCols = kTmemUse <= 128 ? 128 : 256;
   static_assert(kDynamic <= 233472 / kBlocks - 1024, "shared memory per block");
   static_assert(kStages >= 3, "ring depth");
-  static_assert(kQ8Scan * 4 == kQ8Threads, "four threads a sum");
+  static_assert(kQ8Scan * 4 <= kQ8Threads, "four threads a sum");
   static_assert(kTmemUse <= kTmemCols && kTmemCols * kBlocks <= 512, "tensor memory");
   static_assert(kR <= 16, "digit rows");
 };
@@ -223,6 +231,19 @@ __device__ __forceinline__ void tmem_ld_cols(uint32_t taddr, uint32_t* r) {
   }
 }
 template <int NC>
+__device__ __forceinline__ void tmem_st_cols(uint32_t taddr, const uint32_t* r) {
+  if constexpr (NC == 1) {
+    asm volatile("tcgen05.st.sync.aligned.32x32b.x1.b32 [%0], {%1};" ::"r"(taddr), "r"(r[0]) : "memory");
+  } else if constexpr (NC == 2) {
+    asm volatile("tcgen05.st.sync.aligned.32x32b.x2.b32 [%0], {%1,%2};" ::"r"(taddr), "r"(r[0]), "r"(r[1]) : "memory");
+  } else {
+    asm volatile("tcgen05.st.sync.aligned.32x32b.x4.b32 [%0], {%1,%2,%3,%4};" ::"r"(taddr), "r"(r[0]), "r"(r[1]),
+                 "r"(r[2]), "r"(r[3])
+                 : "memory");
+    if constexpr (NC > 4) tmem_st_cols<NC - 4>(taddr + 4, r + 4);
+  }
+}
+template <int NC>
 __device__ __forceinline__ void reg_fence(uint32_t* r) {
 #pragma unroll
   for (int i = 0; i < NC; ++i) asm volatile("" : "+r"(r[i]));
@@ -231,7 +252,7 @@ __device__ __forceinline__ void reg_fence(uint32_t* r) {
 // Warp maximum that keeps a NaN, and the maximum of two values that keeps a NaN.
 __device__ __forceinline__ float warp_max_nan(float x) {
   float y;
-  asm volatile("redux.sync.max.NaN.f32 %0, %1, 0xffffffff;" : "=f"(y) : "f"(x));
+  asm("redux.sync.max.NaN.f32 %0, %1, 0xffffffff;" : "=f"(y) : "f"(x));
   return y;
 }
 __device__ __forceinline__ float max_nan(float a, float b) {
@@ -301,8 +322,11 @@ __global__ void __launch_bounds__(kQ8Threads, DecodeQ8Smem<D, NH, GP, I8>::kBloc
   uint64_t* p_ready = s_free + 2;    // [2]
   uint64_t* o_full = p_ready + 2;    // [2]
   uint64_t* q_ready = o_full + 2;    // [2]
-  uint64_t* ml_ready = q_ready + 2;
-  uint64_t* done = ml_ready + 1;     // [2]
+  uint64_t* ml_ready = q_ready + 2;  // [2]
+  uint64_t* done = ml_ready + 2;     // [2]
+  uint64_t* y_ready = done + 2;      // [2]
+  uint64_t* swap_full = y_ready + 2;
+  uint64_t* swap_free = swap_full + 1;
   __shared__ int abort_word;
   __shared__ uint32_t tmem_slot;
   volatile int* abort_flag = &abort_word;
@@ -315,7 +339,7 @@ __global__ void __launch_bounds__(kQ8Threads, DecodeQ8Smem<D, NH, GP, I8>::kBloc
   // an int: sequences of 2^30 tokens would need block tables of terabytes first.)
   const int per_entry = (p.num_seqs + kQ8Scan - 1) / kQ8Scan;
   const int scan_at = (threadIdx.x >> 2) * per_entry + (threadIdx.x & 3);
-  const int scan_end = min((int(threadIdx.x >> 2) + 1) * per_entry, p.num_seqs);
+  const int scan_end = threadIdx.x < 4 * kQ8Scan ? min((int(threadIdx.x >> 2) + 1) * per_entry, p.num_seqs) : 0;
   int first_len = scan_at < scan_end ? __ldg(&p.seq_lens[scan_at]) : 0;
   // the first 32 lengths, which the K warp walks if its work starts there
   const int window0 = warp == kQ8KWarp && lane < p.num_seqs ? __ldg(&p.seq_lens[lane]) : 0;
@@ -334,12 +358,14 @@ __global__ void __launch_bounds__(kQ8Threads, DecodeQ8Smem<D, NH, GP, I8>::kBloc
       mbar_init(&o_full[i], 1);
       mbar_init(&q_ready[i], 1);
       mbar_init(&done[i], 1);
-      if (i == 0) mbar_init(ml_ready, kQ8SoftmaxWarps);
+      mbar_init(&ml_ready[i], kQ8SoftmaxWarps);
+      mbar_init(&y_ready[i], kQ8SoftmaxWarps);
+      mbar_init(i == 0 ? swap_full : swap_free, kQ8SoftmaxWarps);
     }
     fence_mbar_init();
-  } else if (warp < kQ8SoftmaxWarps) {
+  } else if (warp < 2 * kQ8SoftmaxWarps) {
     // digit rows that no query head uses stay zero (q and P digits follow one another)
-    for (int i = threadIdx.x * 16; i < 2 * (L::kQTile + L::kPTile); i += kQ8SoftmaxWarps * 32 * 16)
+    for (int i = threadIdx.x * 16; i < 2 * (L::kQTile + L::kPTile); i += 2 * kQ8SoftmaxWarps * 32 * 16)
       *reinterpret_cast<uint4*>(smem + L::kQT + i) = make_uint4(0, 0, 0, 0);
     fence_proxy_async_smem();
   } else if (lane == 0) {
@@ -355,7 +381,7 @@ __global__ void __launch_bounds__(kQ8Threads, DecodeQ8Smem<D, NH, GP, I8>::kBloc
     }
     sum += __shfl_xor_sync(0xffffffffu, sum, 1);
     sum += __shfl_xor_sync(0xffffffffu, sum, 2);
-    if ((threadIdx.x & 3) == 0) scan[threadIdx.x >> 2] = sum;
+    if ((threadIdx.x & 3) == 0 && threadIdx.x < 4 * kQ8Scan) scan[threadIdx.x >> 2] = sum;
   }
   if (warp == kQ8ScoreWarp) {
     tmem_alloc(&tmem_slot, L::kTmemCols);
@@ -366,10 +392,11 @@ __global__ void __launch_bounds__(kQ8Threads, DecodeQ8Smem<D, NH, GP, I8>::kBloc
   tc_fence_after();
   const uint32_t tmem = tmem_slot;
   const uint32_t tmem_s = tmem;                    // two buffers of kSBuf columns
-  const uint32_t tmem_o = tmem + 2 * L::kSBuf;     // two buffers of four groups of KN columns, one per softmax warp
+  const uint32_t tmem_o = tmem + 2 * L::kSBuf;     // two buffers of KN columns
 
   if (warp == kQ8KWarp) {
     // ------------------------------------------------------------ producer warp: work, K, scales
+    setmaxnreg_dec<L::kHelperRegs>();
     const int c = lane & 7;            // lane: chunk c of the tile; bit 3: V scales; bit 4: second head of the row
     const bool box_lane = lane < 8 && (c & (p.box / kQ8Chunk - 1)) == 0;   // lane of a copy's first chunk
     const float* sc_src = (lane & 8) ? p.v_scales : p.k_scales;
@@ -436,6 +463,7 @@ __global__ void __launch_bounds__(kQ8Threads, DecodeQ8Smem<D, NH, GP, I8>::kBloc
     uint32_t phase = 0;
     uint32_t pending = 0, pending_phase = 0;
     bool ok = true, fetch = true;
+    int part_no = -1;
     for (;;) {
       if (fetch) {
         fetch = false;
@@ -463,6 +491,7 @@ __global__ void __launch_bounds__(kQ8Threads, DecodeQ8Smem<D, NH, GP, I8>::kBloc
       if (t0 >= w.t_end) {   // the next part
         if (nx.n == 0) break;
         w = nx;
+        ++part_no;
         t0 = w.t_begin;
         page = nx_page;
         row = w.grp * p.team + team_lane;                // 128-byte row of the tokens
@@ -494,6 +523,9 @@ __global__ void __launch_bounds__(kQ8Threads, DecodeQ8Smem<D, NH, GP, I8>::kBloc
       const bool first = t0 == w.t_begin;
       int* job = reinterpret_cast<int*>(smem + L::kJob) + slot * 12;
       ok = __all_sync(0xffffffffu, q8_wait(&empty[slot], phase ^ 1u, abort_flag, p.status));
+      // the query rows of the part before the previous one have been turned into digits
+      if (first && part_no >= 2)
+        ok = __all_sync(0xffffffffu, ok && q8_wait(&q_ready[part_no & 1], uint32_t((part_no - 2) >> 1) & 1u, abort_flag, p.status));
       if (!ok) break;
       if (lane < 8) job[lane] = page;
       if (lane == 0) {
@@ -504,13 +536,15 @@ __global__ void __launch_bounds__(kQ8Threads, DecodeQ8Smem<D, NH, GP, I8>::kBloc
         ti.seq = w.seq; ti.split = part; ti.kvh = row; ti.t0 = t0;
         ti.ntok = ntok;
         ti.bad = int(~good_mask & 0xFFu);
-        ti.flags = (first ? 1 : 0) | (t0 + kQ8Tok >= w.t_end ? 2 : 0);
-        ti.len = 0;
+        // 1: first tile of the part; 2: last; 8: its warpgroup's last of the part; 16: the part has several
+        ti.flags = (first ? 1 : 0) | (t0 + kQ8Tok >= w.t_end ? 2 : 0) | (t0 + 2 * kQ8Tok >= w.t_end ? 8 : 0) |
+                   (w.n > 1 ? 16 : 0);
+        ti.len = part_no;
         info[slot] = ti;
         const uint32_t qbytes = first ? uint32_t(q_rows * D * 2) : 0u;
         mbar_arrive_expect_tx(&full[slot], uint32_t(__popc(box_mask)) * uint32_t(2 * kQ8Row * p.box) + qbytes);
         if (first)
-          bulk_load(smem + L::kQRows + slot * L::kQBytes, p.q + (size_t(w.seq) * p.Hq + size_t(head0) * p.G) * D, qbytes,
+          bulk_load(smem + L::kQRows + (part_no & 1) * L::kQBytes, p.q + (size_t(w.seq) * p.Hq + size_t(head0) * p.G) * D, qbytes,
                     &full[slot]);
       }
       __syncwarp();
@@ -528,8 +562,10 @@ __global__ void __launch_bounds__(kQ8Threads, DecodeQ8Smem<D, NH, GP, I8>::kBloc
       fetch = first;
     }
     if (lane == 0) p.ws_cut[blockIdx.x] = cut;
-    if (ok && __all_sync(0xffffffffu, q8_wait(&empty[slot], phase ^ 1u, abort_flag, p.status))) {
-      if (lane == 0) {   // end-of-work marker: a stage with no copies
+    for (int i = 0; i < 2 && ok; ++i) {   // end-of-work markers, one for each warpgroup: stages with no copies
+      ok = __all_sync(0xffffffffu, q8_wait(&empty[slot], phase ^ 1u, abort_flag, p.status));
+      if (!ok) break;
+      if (lane == 0) {
         TileInfo ti{};
         ti.flags = 4;
         info[slot] = ti;
@@ -539,8 +575,7 @@ __global__ void __launch_bounds__(kQ8Threads, DecodeQ8Smem<D, NH, GP, I8>::kBloc
       }
       __syncwarp();
       cp_async_arrive_noinc(&full[slot]);
-    } else {
-      ok = false;
+      if (++slot == NS) { slot = 0; phase ^= 1u; }
     }
     cp_async_wait_all();
     if (!ok && lane == 0) {
@@ -549,6 +584,7 @@ __global__ void __launch_bounds__(kQ8Threads, DecodeQ8Smem<D, NH, GP, I8>::kBloc
     }
   } else if (warp == kQ8VWarp) {
     // ------------------------------------------------------------ producer warp: V, as the first one says
+    setmaxnreg_dec<L::kHelperRegs>();
     int slot = 0;
     uint32_t phase = 0;
     while (__all_sync(0xffffffffu, q8_wait(&v_go[slot], phase, abort_flag, p.status))) {
@@ -566,6 +602,7 @@ __global__ void __launch_bounds__(kQ8Threads, DecodeQ8Smem<D, NH, GP, I8>::kBloc
     }
   } else if (warp == kQ8ScoreWarp) {
     // ------------------------------------------------------------ query digits and score products
+    setmaxnreg_dec<L::kHelperRegs>();
     constexpr uint32_t idesc_s = make_idesc_q8<I8>(kQ8Tok, KN, 0);   // K tile: rows = tokens, K-major
     const uint64_t q_desc0 = make_sdesc_rows(smem_u32(smem + L::kQT));
     const uint64_t k_desc0 = make_sdesc_rows(smem_u32(smem));
@@ -591,7 +628,7 @@ __global__ void __launch_bounds__(kQ8Threads, DecodeQ8Smem<D, NH, GP, I8>::kBloc
           const int i = min(i0 + (lane >> 3), n_rows - 1);   // a repeated last row writes the same again
           const int nh = NH == 2 && i >= p.G ? 1 : 0;
           const int r = nh * GP + (i - nh * p.G);            // digit row
-          const uint4* src = reinterpret_cast<const uint4*>(smem + L::kQRows + slot * L::kQBytes + (i * D + part8 * E) * 2);
+          const uint4* src = reinterpret_cast<const uint4*>(smem + L::kQRows + qb * L::kQBytes + (i * D + part8 * E) * 2);
           uint32_t w[E / 2];
           uint32_t top = 0;
 #pragma unroll
@@ -664,6 +701,7 @@ __global__ void __launch_bounds__(kQ8Threads, DecodeQ8Smem<D, NH, GP, I8>::kBloc
     __syncwarp();
   } else if (warp == kQ8PvWarp) {
     // ------------------------------------------------------------ P V products (one thread)
+    setmaxnreg_dec<L::kHelperRegs>();
     if (lane == 0) {
       constexpr uint32_t idesc_o = make_idesc_q8<I8>(kQ8Row, KN, 1);   // V tile: rows = head dims, MN-major
       const uint64_t p_desc0 = make_sdesc_rows(smem_u32(smem + L::kPT));
@@ -677,8 +715,8 @@ __global__ void __launch_bounds__(kQ8Threads, DecodeQ8Smem<D, NH, GP, I8>::kBloc
         const uint64_t v_desc = v_desc0 + uint64_t(slot * (L::kStageBytes >> 4));
         const uint64_t p_desc = p_desc0 + uint64_t(pb * (L::kPTile >> 4));
 #pragma unroll
-        for (int w = 0; w < 4; ++w)   // O^T_w: tokens 32w .. 32w + 31
-          umma_q8<I8>(tmem_o + (pb * 4 + w) * KN, v_desc + uint64_t(w * (32 * kQ8Row >> 4)), p_desc + 2 * w, idesc_o, 0);
+        for (int w = 0; w < 4; ++w)   // tokens 32w .. 32w + 31
+          umma_q8<I8>(tmem_o + pb * KN, v_desc + uint64_t(w * (32 * kQ8Row >> 4)), p_desc + 2 * w, idesc_o, w > 0);
         umma_commit(&o_full[pb]);
         umma_commit(&empty[slot]);    // the tile's products are done with its K and V
         if (++slot == NS) { slot = 0; phase ^= 1u; }
@@ -691,83 +729,47 @@ __global__ void __launch_bounds__(kQ8Threads, DecodeQ8Smem<D, NH, GP, I8>::kBloc
     __syncwarp();
   } else {
     // ------------------------------------------------------------ softmax warps: thread = token, then head dim
+    setmaxnreg_inc<L::kSoftmaxRegs>();
     const float neg_inf = -__int_as_float(0x7f800000);
-    const uint32_t lane_base = uint32_t(warp * 32) << 16;
-    const int tok = warp * 32 + lane;         // also the byte of the row whose O this thread holds
-    const int my_half = NH == 2 ? warp >> 1 : 0;
-    float* alpha = reinterpret_cast<float*>(smem + L::kAlpha);
-    float* ml = reinterpret_cast<float*>(smem + L::kMl);
-    const float* qf_s = reinterpret_cast<const float*>(smem + L::kQf);
+    // running maxima start below every score that is not -inf, and are finite, so that differences are numbers
+    constexpr float kFloor = -3.402823466e38f;
+    const int wg = warp >> 2, ww = warp & 3;
+    const uint32_t lane_base = uint32_t(ww * 32) << 16;
+    const int tok = ww * 32 + lane;           // also the byte of the row whose O this thread holds
+    const int my_half = NH == 2 ? ww >> 1 : 0;
+    float* ml = reinterpret_cast<float*>(smem + L::kMl) + wg * (4 * R * 2);
     constexpr float kPScale = I8 ? 32512.f : 256.f;   // 127 * 256: both digits stay inside int8
-    int slot = 0, tile = 0, item_no = 0;
-    uint32_t phase = 0, m_ph = 0;
+    const uint32_t my_s = tmem_s + wg * L::kSBuf + lane_base;
+    const uint32_t my_o = tmem_o + wg * KN + lane_base + my_half * GP;
+    const uint32_t my_swap = tmem + L::kTmemSwap + lane_base;
+    uint8_t* p_tile = smem + L::kPT + wg * L::kPTile;
+    int slot = wg;                            // tiles wg, wg + 2, ... of the CTA
+    uint32_t phase = 0, t_ph = 0, m_ph = 0, x_ph = 0;
     bool ok = true;
-    int seq = 0, part = 0, row = 0;
-    float qf[R], X[R], Y[R], l[R];
-    float o[4][GP];
+    int part_no = -1;
+    float X[R], Y[R], l[R];   // X of this warp's tokens, Y of the warpgroup's, l of this thread's
+    float o[GP];
 #pragma unroll
-    for (int h = 0; h < R; ++h) { qf[h] = 0.f; X[h] = Y[h] = neg_inf; l[h] = 0.f; }
+    for (int h = 0; h < R; ++h) { X[h] = Y[h] = kFloor; l[h] = 0.f; }
 #pragma unroll
-    for (int h = 0; h < GP; ++h) o[0][h] = o[1][h] = o[2][h] = o[3][h] = 0.f;
+    for (int h = 0; h < GP; ++h) o[h] = 0.f;
     auto wait = [&](uint64_t* bar, uint32_t ph) -> bool {   // the same answer in the whole warp
       return __all_sync(0xffffffffu, q8_wait(bar, ph, abort_flag, p.status));
     };
-    // O^T of tile number t: thread = head dimension, one accumulator per warp's tokens
-    auto add_tile = [&](int t) -> bool {
-      const int b = t & 1;
-      const uint32_t ph = uint32_t(t >> 1) & 1u;
-      if (!wait(&p_ready[b], ph) || !wait(&o_full[b], ph)) return false;   // every warp's factors; the products
-      tc_fence_after();
-      const float* al = alpha + (t & 3) * 4 * R + my_half * GP;
-      constexpr int WB = GP <= 4 ? 4 : 2;   // accumulator groups read together
-#pragma unroll
-      for (int w0 = 0; w0 < 4; w0 += WB) {
-        uint32_t hi[WB][GP], lo[WB][GP];
-#pragma unroll
-        for (int w = 0; w < WB; ++w) {
-          const uint32_t at = tmem_o + (b * 4 + w0 + w) * KN + lane_base + my_half * GP;
-          tmem_ld_cols<GP>(at, hi[w]);
-          tmem_ld_cols<GP>(at + R, lo[w]);
-        }
-        tmem_ld_wait();
-#pragma unroll
-        for (int w = 0; w < WB; ++w) {
-          reg_fence<GP>(hi[w]);
-          reg_fence<GP>(lo[w]);
-#pragma unroll
-          for (int h = 0; h < GP; ++h)
-            o[w0 + w][h] = fmaf(o[w0 + w][h], al[(w0 + w) * R + h], join_digits<I8>(hi[w][h], lo[w][h]));
-        }
-      }
-      tc_fence_before();
-      return true;
-    };
-
-    bool drain = false;   // the part's last tile has been weighted; its O^T is still to be added
     while (ok) {
-     bool first = false, last = false;
-     if (!drain) {
-      const int sb = tile & 1;
-      const uint32_t t_ph = uint32_t(tile >> 1) & 1u;   // this tile's use of its double buffers
       if (!wait(&full[slot], phase)) { ok = false; break; }
+      const int flags = info[slot].flags;
+      if (flags & 4) break;
       const TileInfo ti = info[slot];
-      if (ti.flags & 4) break;
       uint8_t* stage = smem + slot * L::kStageBytes;
-      first = (ti.flags & 1) != 0;
-      last = (ti.flags & 2) != 0;
-      if (first) {
-        seq = ti.seq; part = ti.split; row = ti.kvh;
-        if (!wait(&q_ready[item_no & 1], uint32_t(item_no >> 1) & 1u)) { ok = false; break; }
-        const float* qs = qf_s + (item_no & 1) * R;
+      const int q_par = ti.len & 1;
+      if (ti.len != part_no) {   // this warpgroup's first tile of the part
+        part_no = ti.len;
+        if (!wait(&q_ready[q_par], uint32_t(part_no >> 1) & 1u)) { ok = false; break; }
 #pragma unroll
-        for (int h = 0; h < R; ++h) {
-          qf[h] = h % GP < p.G ? qs[h] : 0.f;
-          X[h] = Y[h] = neg_inf;
-          l[h] = 0.f;
-        }
+        for (int h = 0; h < R; ++h) { X[h] = Y[h] = kFloor; l[h] = 0.f; }
 #pragma unroll
-        for (int h = 0; h < GP; ++h) o[0][h] = o[1][h] = o[2][h] = o[3][h] = 0.f;
-        ++item_no;
+        for (int h = 0; h < GP; ++h) o[h] = 0.f;
       }
       const bool valid = tok < ti.ntok && !((ti.bad >> (tok >> 4)) & 1);
       if (!valid) {   // a V row that was not copied: 0 * (stale bytes) must not reach O
@@ -779,46 +781,75 @@ __global__ void __launch_bounds__(kQ8Threads, DecodeQ8Smem<D, NH, GP, I8>::kBloc
 #pragma unroll
       for (int n = 0; n < NH; ++n) {
         ks[n] = scales[slot * 16 * NH + n * 16 + (tok >> 4)];
-        lvs[n] = __log2f(scales[slot * 16 * NH + n * 16 + 8 + (tok >> 4)]);
+        const float vs = scales[slot * 16 * NH + n * 16 + 8 + (tok >> 4)];
+        lvs[n] = valid ? __log2f(vs) : 0.f;   // an absent token's scale was not copied
+      }
+      float xs[R];
+      {
+        const float* qs = reinterpret_cast<const float*>(smem + L::kQf) + q_par * R;
+#pragma unroll
+        for (int h = 0; h < R; ++h) xs[h] = (h % GP < p.G ? qs[h] : 0.f) * ks[h / GP];
       }
 
       // ---- scores of this token for all heads
-      if (!wait(&s_full[sb], t_ph)) { ok = false; break; }
+      if (!wait(&s_full[wg], t_ph)) { ok = false; break; }
       tc_fence_after();
-      uint32_t s_hi[R], s_lo[R];
+      {
+        uint32_t s_hi[R], s_lo[R];
 #pragma unroll
-      for (int n = 0; n < NH; ++n) {
-        const uint32_t at = tmem_s + sb * L::kSBuf + n * KN + lane_base + n * GP;
-        tmem_ld_cols<GP>(at, s_hi + n * GP);
-        tmem_ld_cols<GP>(at + R, s_lo + n * GP);
+        for (int n = 0; n < NH; ++n) {
+          tmem_ld_cols<GP>(my_s + n * KN + n * GP, s_hi + n * GP);
+          tmem_ld_cols<GP>(my_s + n * KN + n * GP + R, s_lo + n * GP);
+        }
+        tmem_ld_wait();
+        reg_fence<R>(s_hi);
+        reg_fence<R>(s_lo);
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&s_free[wg]);
+#pragma unroll
+        for (int h = 0; h < R; ++h) xs[h] = valid ? join_digits<I8>(s_hi[h], s_lo[h]) * xs[h] : neg_inf;
       }
-      tmem_ld_wait();
-      reg_fence<R>(s_hi);
-      reg_fence<R>(s_lo);
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&s_free[sb]);
-      float pv[R];
+      // ---- maxima: of y over the warpgroup's 128 tokens, of x over this warp's
+      float* ymax = reinterpret_cast<float*>(smem + L::kYmax) + (wg * 2 + t_ph) * 4 * R;   // [row][warp]
 #pragma unroll
       for (int h = 0; h < R; ++h) {
-        const float x = valid ? join_digits<I8>(s_hi[h], s_lo[h]) * (qf[h] * ks[h / GP]) : neg_inf;
-        const float y = valid ? x + lvs[h / GP] : neg_inf;
-        const float nx = max_nan(X[h], warp_max_nan(x)), ny = max_nan(Y[h], warp_max_nan(y));
-        const float offx = nx == neg_inf ? 0.f : nx, offy = ny == neg_inf ? 0.f : ny;
-        l[h] = fmaf(l[h], fast_exp2(X[h] - offx), fast_exp2(x - offx));
-        pv[h] = fast_exp2(y - offy) * kPScale;
-        if (lane == 0) alpha[((tile & 3) * 4 + warp) * R + h] = fast_exp2(Y[h] - offy);
-        X[h] = nx;
-        Y[h] = ny;
+        const float ty = warp_max_nan(xs[h] + lvs[h / GP]);
+        if (lane == 0) ymax[4 * h + ww] = ty;
+      }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&y_ready[wg]);
+#pragma unroll
+      for (int h = 0; h < R; ++h) {
+        const float tx = max_nan(X[h], warp_max_nan(xs[h]));
+        if (!(tx == X[h])) {   // it grew (or is a NaN); the same in the whole warp
+          l[h] *= fast_exp2(X[h] - tx);
+          X[h] = tx;
+        }
+        l[h] += fast_exp2(xs[h] - X[h]);
+      }
+      if (!wait(&y_ready[wg], t_ph)) { ok = false; break; }
+#pragma unroll
+      for (int h = 0; h < R; ++h) {
+        const float4 t = *reinterpret_cast<const float4*>(ymax + 4 * h);
+        const float ty = max_nan(Y[h], max_nan(max_nan(t.x, t.y), max_nan(t.z, t.w)));
+        if (!(ty == Y[h])) {   // the same in the whole warpgroup
+          const float a = fast_exp2(Y[h] - ty);
+          Y[h] = ty;
+          if (NH == 1 || h / GP == my_half) o[h % GP] *= a;
+        }
       }
       // ---- P digits: row h (hi) and R + h (lo), this token's byte
       {
-        uint8_t* p_tile = smem + L::kPT + sb * L::kPTile;
-        const int unit = 2 * warp + (lane >> 4), b = lane & 15;
+        const int unit = 2 * ww + (lane >> 4), b = lane & 15;
 #pragma unroll
         for (int h = 0; h < R; h += 2) {
+          float pv[2] = {0.f, 0.f};
+#pragma unroll
+          for (int k = 0; k < 2 && h + k < R; ++k)
+            pv[k] = fast_exp2(xs[h + k] + lvs[(h + k) / GP] - Y[h + k]) * kPScale;
           uint32_t hi, lo;
-          two_digits<I8>(pv[h], h + 1 < R ? pv[h + 1 < R ? h + 1 : h] : 0.f, hi, lo);
+          two_digits<I8>(pv[0], pv[1], hi, lo);
           p_tile[row_unit(h, unit) + b] = uint8_t(hi);
           p_tile[row_unit(R + h, unit) + b] = uint8_t(lo);
           if (h + 1 < R) {
@@ -830,71 +861,102 @@ __global__ void __launch_bounds__(kQ8Threads, DecodeQ8Smem<D, NH, GP, I8>::kBloc
       fence_proxy_async_smem();
       tc_fence_before();
       __syncwarp();
-      if (lane == 0) mbar_arrive(&p_ready[sb]);
+      if (lane == 0) mbar_arrive(&p_ready[wg]);
 
-     }
-      if ((drain || !first) && !add_tile(tile - 1)) { ok = false; break; }
-      if (!drain) {
-        if (++slot == NS) { slot = 0; phase ^= 1u; }
-        ++tile;
-        drain = last;
-        continue;
+      // ---- O^T of the tile: thread = head dimension
+      if (!wait(&o_full[wg], t_ph)) { ok = false; break; }
+      tc_fence_after();
+      {
+        uint32_t hi[GP], lo[GP];
+        tmem_ld_cols<GP>(my_o, hi);
+        tmem_ld_cols<GP>(my_o + R, lo);
+        tmem_ld_wait();
+        reg_fence<GP>(hi);
+        reg_fence<GP>(lo);
+#pragma unroll
+        for (int h = 0; h < GP; ++h) o[h] += join_digits<I8>(hi[h], lo[h]);
+        tc_fence_before();
       }
-      drain = false;
+      slot += 2;
+      if (slot >= NS) { slot -= NS; phase ^= 1u; }
+      t_ph ^= 1u;
+      if (!(flags & 8)) continue;
 
-      // ---- the part's result: the four warps' accumulators onto common maxima
+      // ---- the part ends for this warpgroup: the sums of its four warps
 #pragma unroll
       for (int h = 0; h < R; ++h) {
 #pragma unroll
         for (int s = 16; s > 0; s >>= 1) l[h] += __shfl_xor_sync(0xffffffffu, l[h], s);
-        if (lane == 0) {
-          float* m = ml + (warp * R + h) * 3;
-          m[0] = X[h]; m[1] = Y[h]; m[2] = l[h];
-        }
+        if (lane == 0) *reinterpret_cast<float2*>(ml + (ww * R + h) * 2) = make_float2(X[h], l[h]);
       }
       __syncwarp();
-      if (lane == 0) mbar_arrive(ml_ready);
-      if (!wait(ml_ready, m_ph)) { ok = false; break; }
+      if (lane == 0) mbar_arrive(&ml_ready[wg]);
+      if (!wait(&ml_ready[wg], m_ph)) { ok = false; break; }
       m_ph ^= 1u;
+      const bool finish = (flags & 2) != 0, swap = (flags & 16) != 0;
+      float* other = reinterpret_cast<float*>(smem + L::kSwap);
+      if (swap && !wait(finish ? swap_full : swap_free, finish ? x_ph : x_ph ^ 1u)) { ok = false; break; }
+      x_ph ^= swap ? 1u : 0u;
+      uint32_t theirs[GP];
+      if (!finish) {
+#pragma unroll
+        for (int h = 0; h < GP; ++h) theirs[h] = __float_as_uint(o[h]);
+        tmem_st_cols<GP>(my_swap, theirs);
+      } else if (swap) {
+        tc_fence_after();
+        tmem_ld_cols<GP>(my_swap, theirs);
+        tmem_ld_wait();
+        reg_fence<GP>(theirs);
+        tc_fence_before();
+      }
+      const int row = ti.kvh, part = ti.split;
       const int head = (NH == 2 ? row * 2 : row) + my_half;   // KV head whose dims this thread may hold
       const int dim = D == 64 ? tok & 63 : tok;
       const bool mine = head < p.Hkv && (D == 128 || NH == 2 || (tok >> 6) == (row & 1));
-      const size_t at0 = part < 0 ? size_t(seq) * p.Hq + size_t(head) * p.G : size_t(part) * p.part_rows + my_half * p.G;
-      // lane 4 h + w: warp w's share of query head h (eight heads at a time)
-      const int w4 = lane & 3;
+      const size_t at0 = part < 0 ? size_t(ti.seq) * p.Hq + size_t(head) * p.G : size_t(part) * p.part_rows + my_half * p.G;
+      const bool writer = (ww & (NH == 2 ? 1 : 3)) == 0 && lane == 0;   // one thread of each head half
 #pragma unroll
-      for (int h0 = 0; h0 < GP; h0 += 8) {
-        const int h = min(h0 + (lane >> 2), GP - 1);
-        const float* m = ml + (w4 * R + my_half * GP + h) * 3;
-        float mx = m[0], my = m[1];
-        mx = max_nan(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
-        my = max_nan(my, __shfl_xor_sync(0xffffffffu, my, 1));
-        mx = max_nan(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
-        my = max_nan(my, __shfl_xor_sync(0xffffffffu, my, 2));
-        const float offx = mx == neg_inf ? 0.f : mx, offy = my == neg_inf ? 0.f : my;
-        float lsum = m[2] * fast_exp2(m[0] - offx);
-        lsum += __shfl_xor_sync(0xffffffffu, lsum, 1);
-        lsum += __shfl_xor_sync(0xffffffffu, lsum, 2);
+      for (int h = 0; h < GP; ++h) {
+        const int r = NH == 2 && my_half ? GP + h : h;   // the row's number, and its Y: not an index of registers
+        const float yh = NH == 2 && my_half ? Y[(NH - 1) * GP + h] : Y[h];
+        float mx = kFloor, lsum = 0.f;
+#pragma unroll
+        for (int w = 0; w < 4; ++w) mx = max_nan(mx, ml[(w * R + r) * 2]);
+        float* sw = other + r * 3;
+        float ox = kFloor, oy = kFloor, ol = 0.f;
+        if (swap && finish) {
+          ox = sw[0]; oy = sw[1]; ol = sw[2];
+          mx = max_nan(mx, ox);
+        }
+#pragma unroll
+        for (int w = 0; w < 4; ++w) lsum = fmaf(ml[(w * R + r) * 2 + 1], fast_exp2(ml[(w * R + r) * 2] - mx), lsum);
+        if (!finish) {
+          if (writer) { sw[0] = mx; sw[1] = yh; sw[2] = lsum; }
+          continue;
+        }
+        lsum = fmaf(ol, fast_exp2(ox - mx), lsum);
+        const float my = max_nan(yh, oy);
+        float v = o[h] * fast_exp2(yh - my);
+        if (swap) v = fmaf(__uint_as_float(theirs[h]), fast_exp2(oy - my), v);
         // lsum is 0 only if every page was invalid; a NaN stays a NaN
-        const float share = lsum == 0.f ? 0.f : __fdividef(fast_exp2(m[1] - offy) * fast_exp2(offy - offx) * (1.f / kPScale), lsum);
-        if (p.lse || part >= 0) {
-          const float lse2 = lsum == 0.f ? neg_inf : mx + __log2f(lsum);
-          // one warp of each head half writes: lane 4 h
-          if ((warp & (NH == 2 ? 1 : 3)) == 0 && w4 == 0 && h0 + (lane >> 2) < p.G && head < p.Hkv) {
-            if (part < 0) p.lse[at0 + h] = lse2 * 0.69314718055994531f;
-            else p.ws_lse[at0 + h] = lse2;
-          }
+        v = lsum == 0.f ? 0.f : __fdividef(v * fast_exp2(my - mx) * (1.f / kPScale), lsum);
+        const float lse2 = lsum == 0.f ? neg_inf : mx + __log2f(lsum);
+        if (h >= p.G || !mine) continue;
+        if (part < 0) {
+          p.o[(at0 + h) * D + dim] = __float2bfloat16_rn(v);
+          if (p.lse && dim == 0) p.lse[at0 + h] = lse2 * 0.69314718055994531f;
+        } else {
+          p.ws_o[(at0 + h) * D + dim] = v;
+          if (dim == 0) p.ws_lse[at0 + h] = lse2;
         }
-#pragma unroll
-        for (int k = 0; k < 8 && k < GP; ++k) {
-          float out = 0.f;
-#pragma unroll
-          for (int w = 0; w < 4; ++w) out = fmaf(o[w][h0 + k], __shfl_sync(0xffffffffu, share, 4 * k + w), out);
-          if (h0 + k < p.G && mine) {
-            if (part < 0) p.o[(at0 + h0 + k) * D + dim] = __float2bfloat16_rn(out);
-            else p.ws_o[(at0 + h0 + k) * D + dim] = out;
-          }
+      }
+      if (swap) {
+        if (!finish) {
+          tmem_st_wait();
+          tc_fence_before();
         }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(finish ? swap_free : swap_full);
       }
     }
   }
