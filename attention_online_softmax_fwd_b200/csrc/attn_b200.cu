@@ -148,15 +148,15 @@ int encode_bshd(CUtensorMap* map, const void* base, int B, int S, int H, int D, 
 
 int launch_status() { return cudaGetLastError() == cudaSuccess ? ATTN_OK : ATTN_ERR_CUDA; }
 
-template <int D, bool CAUSAL, bool SKIP, bool PAGED = false, bool DBG = false>
+template <int D, bool CAUSAL, bool SKIP, bool PAGED = false, bool DBG = false, bool CONTIG = false>
 int launch_prefill(const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv, const CUtensorMap& tvh,
                    const PrefillParams& p, int sms, cudaStream_t stream) {
-  auto kernel = prefill_kernel<D, CAUSAL, SKIP, PAGED, DBG>;
+  auto kernel = prefill_kernel<D, CAUSAL, SKIP, PAGED, DBG, CONTIG>;
   constexpr int smem = PrefillSmem<D>::kDynamic;
   // The kernel moves registers between warpgroups with setmaxnreg; the block's
   // launch allocation must cover the split or the increase would never return
   // (checked with the shared-memory limit, once per device).
-  if (int st = set_smem_once<prefill_kernel<D, CAUSAL, SKIP, PAGED, DBG>>(
+  if (int st = set_smem_once<prefill_kernel<D, CAUSAL, SKIP, PAGED, DBG, CONTIG>>(
           smem, (kPfRegPoolNeeded + kPfThreads - 1) / kPfThreads))
     return st;
   const long long grid = p.num_items < sms ? p.num_items : sms;
@@ -692,23 +692,21 @@ int check_q8_pool(const void* k_codes, const void* v_codes, const float* k_scale
   return ATTN_OK;
 }
 
-// Workspace of the prefill over an 8-bit cache, parts 256-byte aligned:
-// [block table of the scratch pages][K pages, bf16][V pages, bf16], num_seqs * max_pages pages each.
+// Workspace of the prefill over an 8-bit cache: bf16 K and V [num_seqs][max_pages * page_size][Hkv][D],
+// V 256-byte aligned behind K.
 struct PrefillQ8Layout {
-  size_t k_off = 0, v_off = 0, total = 0;
+  size_t v_off = 0, total = 0;
 };
 bool prefill_q8_layout(int num_seqs, int Hkv, int D, int page_size, int max_pages, PrefillQ8Layout* L) {
   if (num_seqs < 1 || Hkv < 1 || (D != 64 && D != 128) || !valid_page_size(page_size) || max_pages < 1) return false;
   if ((long long)num_seqs * max_pages > 0x7fffffffll) return false;
   const size_t pages = size_t(num_seqs) * size_t(max_pages);
-  size_t pool = 0, k_off = 0, v_off = 0, end = 0;
-  if (!mul_size(pages, size_t(page_size) * size_t(D) * 2, &pool) || !mul_size(pool, size_t(Hkv), &pool)) return false;
-  if (!add_size(pages * sizeof(int32_t), 255, &k_off)) return false;
-  k_off = k_off / 256 * 256;
-  if (!add_size(k_off, pool, &v_off) || !add_size(v_off, 255, &v_off)) return false;
+  size_t kv = 0, v_off = 0, end = 0;
+  if (!mul_size(pages, size_t(page_size) * size_t(D) * 2, &kv) || !mul_size(kv, size_t(Hkv), &kv)) return false;
+  if (!add_size(kv, 255, &v_off)) return false;
   v_off = v_off / 256 * 256;
-  if (!add_size(v_off, pool, &end)) return false;
-  L->k_off = k_off; L->v_off = v_off; L->total = end;
+  if (!add_size(v_off, kv, &end)) return false;
+  L->v_off = v_off; L->total = end;
   return true;
 }
 
@@ -1253,18 +1251,38 @@ int attn_prefill_paged_q8(const void* q, const void* k_codes, const void* v_code
   p.v_scales = v_scales;
   p.block_table = block_table;
   p.seq_lens = seq_lens;
-  p.k_out = reinterpret_cast<__nv_bfloat16*>(ws + L.k_off);
+  p.k_out = reinterpret_cast<__nv_bfloat16*>(ws);
   p.v_out = reinterpret_cast<__nv_bfloat16*>(ws + L.v_off);
-  p.identity = reinterpret_cast<int32_t*>(ws);
   p.status = device_status;
   p.N = B; p.T = max_pages_per_seq * page_size; p.Hkv = Hkv;
   p.min_len = Sq;
+  p.pad = kPfKeys;   // the rest of a sequence's last tile reads as zeros
   p.max_pages = max_pages_per_seq; p.num_pages = num_pages;
   p.page_shift = log2_of(page_size);
   p.block_shift = log2_of(scale_block);
-  if (int st = launch_read_q8(format, D, p, sms, static_cast<cudaStream_t>(stream))) return st;
-  return attn_prefill_paged(q, ws + L.k_off, ws + L.v_off, p.identity, seq_lens, o, lse, B, Sq, Hq, Hkv, D, page_size,
-                            max_pages_per_seq, B * max_pages_per_seq, scale, device_status, stream);
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  PrefillParams f{};
+  f.o = static_cast<__nv_bfloat16*>(o);
+  f.lse = lse;
+  f.status = device_status;
+  f.B = B; f.S = Sq; f.Hq = Hq; f.Hkv = Hkv;
+  f.n_qblocks = (Sq + 2 * kPfRows - 1) / (2 * kPfRows);
+  f.n_qt = (Sq + kPfRows - 1) / kPfRows;
+  f.num_items = f.n_qblocks * B * Hq;   // fits, checked above
+  f.scale_log2 = scale * 1.4426950408889634f;
+  f.log2_lambda = -INFINITY;
+  f.seq_lens = seq_lens;
+  f.max_pages = max_pages_per_seq;
+  f.page_size = page_size;
+  f.wait_ns = kWaitLimitNs;
+  f.withhold_step = -1;
+  CUtensorMap tq, tk, tv;
+  if (int st = encode_bshd(&tq, q, B, Sq, Hq, D)) return st;
+  if (int st = encode_bshd(&tk, p.k_out, B, p.T, Hkv, D)) return st;
+  if (int st = encode_bshd(&tv, p.v_out, B, p.T, Hkv, D)) return st;
+  if (int st = launch_read_q8(format, D, p, sms, s)) return st;
+  return D == 128 ? launch_prefill<128, true, false, true, false, true>(tq, tk, tv, tv, f, sms, s)
+                  : launch_prefill<64, true, false, true, false, true>(tq, tk, tv, tv, f, sms, s);
 }
 
 }  // extern "C"

@@ -224,10 +224,10 @@ struct KvReadQ8Params {
   const int32_t* seq_lens;      // [N]
   __nv_bfloat16* k_out;         // [N][T][Hkv][D]
   __nv_bfloat16* v_out;
-  int32_t* identity;            // [N][max_pages] or null: entry (b, i) = b * max_pages + i for the pages in use
   int* status;
   int N, T, Hkv, max_pages, num_pages;
   int min_len;                  // rows read even of a shorter sequence (the chunk of a prefill; 0 otherwise)
+  int pad;                      // rows up to the next multiple of this are set to zero (0: left as they were)
   int page_shift, block_shift;
   int group_shift;              // log2(lanes of a row): the power of two >= its 8-code vectors, at most 32
   int ctas_per_seq;
@@ -257,19 +257,15 @@ __global__ void __launch_bounds__(256) kv_read_q8_kernel(const KvReadQ8Params p)
   if (threadIdx.x == 0 && part == 0 && (len < 0 || (len - 1) >> p.page_shift >= p.max_pages))
     raise_status(p.status, ATTN_ERR_DEVICE_BOUNDS);
   const int32_t* table = p.block_table + size_t(b) * p.max_pages;
-  if (p.identity) {
-    const int pages = (held + (1 << p.page_shift) - 1) >> p.page_shift;
-    for (int i = part * 256 + threadIdx.x; i < pages; i += p.ctas_per_seq * 256)
-      p.identity[size_t(b) * p.max_pages + i] = b * p.max_pages + i;
-  }
+  const int stop = p.pad ? min((held + p.pad - 1) / p.pad * p.pad, p.T) : held;
   const int vecs = p.Hkv * (D / 8);                     // 8-code vectors of a row
   const int group = 1 << p.group_shift;                 // lanes of a row
   const int v0 = threadIdx.x & (group - 1);
   const int rows = 256 >> p.group_shift;                // rows of a CTA at a time
-  for (long long t = (long long)part * rows + (threadIdx.x >> p.group_shift); t < held; t += (long long)p.ctas_per_seq * rows) {
-    const int page = __ldg(&table[t >> p.page_shift]);
+  for (long long t = (long long)part * rows + (threadIdx.x >> p.group_shift); t < stop; t += (long long)p.ctas_per_seq * rows) {
+    const int page = t < held ? __ldg(&table[t >> p.page_shift]) : -1;
     const bool good = page >= 0 && page < p.num_pages;
-    if (!good && v0 == 0) raise_status(p.status, ATTN_ERR_DEVICE_BOUNDS);
+    if (!good && v0 == 0 && t < held) raise_status(p.status, ATTN_ERR_DEVICE_BOUNDS);
     const int slot = int(t) & ((1 << p.page_shift) - 1);
     const size_t row = ((size_t(good ? page : 0) << p.page_shift) + slot) * vecs;
     const size_t srow = ((size_t(good ? page : 0) << (p.page_shift - p.block_shift)) + (slot >> p.block_shift)) * p.Hkv;

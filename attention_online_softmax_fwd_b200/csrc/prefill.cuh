@@ -375,10 +375,14 @@ __device__ __forceinline__ int pf_count_skipped(const PrefillParams& p, int jt, 
 // {D, Hkv, page_size, P} with 16-slot boxes).
 // SKIP: tm_vh maps V with boxes of 64 rows (one 64-key half of a tile), so that
 // the producer loads only the halves that one of the two query tiles keeps.
+// CONTIG (with PAGED): the sequences' lengths are those of PAGED, but their keys and
+// values lie in order in one tensor [B][capacity][Hkv][D] (tm_k / tm_v as in the
+// unpaged prefill), so a tile is D / 64 copies instead of D / 8: the 32 copies of a
+// K/V tile pair from 16-token pages take longer to issue than its products.
 // DBG (the test entry point only): the producer's and issuers' wait limit comes
 // from p.wait_ns and the producer leaves out ring step p.withhold_step; every
 // other instantiation waits up to kWaitLimitNs and withholds nothing.
-template <int D, bool CAUSAL, bool SKIP, bool PAGED = false, bool DBG = false>
+template <int D, bool CAUSAL, bool SKIP, bool PAGED = false, bool DBG = false, bool CONTIG = false>
 __global__ void __launch_bounds__(kPfThreads, 1)
     prefill_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
                    const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ CUtensorMap tm_vh,
@@ -516,7 +520,7 @@ __global__ void __launch_bounds__(kPfThreads, 1)
   // (kPfRegPoolNeeded is checked against the launch allocation on the host).
   if (warp < 4) {
     setmaxnreg_dec<kPfRegsLow>();
-    if (warp == kPfProducerWarp && PAGED) {
+    if (warp == kPfProducerWarp && PAGED && !CONTIG) {
       // ============================================================ TMA producer (paged)
       // Lane 0 waits for free slots and arms the barriers; lanes 0-7 each copy
       // one 16-key group of a tile, so the block-table loads and the copies of a

@@ -408,13 +408,13 @@ int attn_decode_paged_q8(const void* q, const void* k_codes, const void* v_codes
 /*
  * attn_prefill_paged_q8 -- attn_prefill_paged over the 8-bit cache: the chunk's
  * queries see the cached keys, end-aligned and causal, the chunk's own included
- * (append them first). The sequences' cache is widened once into bf16 pages in
+ * (append them first). The sequences' cache is widened once into bf16 tensors in
  * the workspace (as attn_kv_read_q8), which the prefill then reads: every query
  * block and head of a group shares that one conversion. Arguments as
  * attn_prefill_paged; the workspace (16-byte aligned, contents ignored) holds at
  * least attn_prefill_paged_q8_workspace_bytes(...) bytes: bf16 K and V of
- * B * max_pages_per_seq pages and a block table, so a table trimmed to the pages
- * in use keeps it small. Returns 0 for invalid arguments or an overflowing size.
+ * B * max_pages_per_seq pages, so a table trimmed to the pages in use keeps it
+ * small. Returns 0 for invalid arguments or an overflowing size.
  */
 size_t attn_prefill_paged_q8_workspace_bytes(int B, int Hkv, int D, int max_pages_per_seq, int page_size);
 int attn_prefill_paged_q8(const void* q, const void* k_codes, const void* v_codes, const float* k_scales,
