@@ -9,6 +9,7 @@ built, every entry point raises :class:`AttnError`; there is no fallback.
 from __future__ import annotations
 
 import ctypes
+import functools
 import math
 import os
 
@@ -402,36 +403,41 @@ def _q8_pool(k_codes, v_codes, k_scales, v_scales, block_table, lens, lens_name)
     """Checks an 8-bit paged cache; returns (format, pages, page_size, Hkv, D, tokens per scale, device index).
 
     Codes are uint8 (E4M3) or int8 [P, page_size, Hkv, D]; scales fp32 [P, page_size / block, Hkv]."""
-    named = (("k_codes", k_codes), ("v_codes", v_codes), ("k_scales", k_scales), ("v_scales", v_scales),
-             ("block_table", block_table), (lens_name, lens))
-    for name, t in named:
-        if not isinstance(t, torch.Tensor):
-            raise AttnError(f"{name}: expected a tensor")
-    kind = k_codes.dtype
-    if kind is not _U8 and kind is not _I8:
-        raise AttnError("k_codes: expected uint8 (E4M3) or int8 codes")
-    shape, sshape = k_codes.shape, k_scales.shape
-    if v_codes.dtype is not kind or k_scales.dtype is not _F32 or v_scales.dtype is not _F32 \
-            or block_table.dtype is not _I32 or lens.dtype is not _I32:
-        raise AttnError("codes must share a type, scales be float32, block_table and lengths int32")
-    if len(shape) != 4 or len(sshape) != 3 or block_table.dim() != 2 or lens.dim() != 1 or v_codes.shape != shape \
-            or v_scales.shape != sshape or sshape[0] != shape[0] or sshape[2] != shape[2] or sshape[1] < 1 \
-            or shape[1] % sshape[1] != 0:
-        raise AttnError("codes must be [P, page_size, Hkv, D] and scales [P, page_size / block, Hkv]")
-    if block_table.shape[0] != lens.shape[0]:
-        raise AttnError(f"block_table and {lens_name} must hold one row and one entry per sequence")
-    dev = k_codes.get_device()
-    for name, t in named:
-        if not t.is_cuda or t.get_device() != dev or not t.is_contiguous():
-            raise AttnError(f"{name}: expected a contiguous CUDA tensor on the cache's device")
-    return (KV_E4M3 if kind is _U8 else KV_INT8), shape[0], shape[1], shape[2], shape[3], shape[1] // sshape[1], dev
+    try:
+        kind, shape, sshape, dev = k_codes.dtype, k_codes.shape, k_scales.shape, k_codes.get_device()
+        if kind is not _U8 and kind is not _I8:
+            raise AttnError("k_codes: expected uint8 (E4M3) or int8 codes")
+        if v_codes.dtype is not kind or k_scales.dtype is not _F32 or v_scales.dtype is not _F32 \
+                or block_table.dtype is not _I32 or lens.dtype is not _I32:
+            raise AttnError("codes must share a type, scales be float32, block_table and lengths int32")
+        if len(shape) != 4 or len(sshape) != 3 or block_table.dim() != 2 or lens.dim() != 1 \
+                or v_codes.shape != shape or v_scales.shape != sshape or sshape[0] != shape[0] \
+                or sshape[2] != shape[2] or sshape[1] < 1 or shape[1] % sshape[1] != 0:
+            raise AttnError("codes must be [P, page_size, Hkv, D] and scales [P, page_size / block, Hkv]")
+        if block_table.shape[0] != lens.shape[0]:
+            raise AttnError(f"block_table and {lens_name} must hold one row and one entry per sequence")
+        if dev < 0 or v_codes.get_device() != dev or k_scales.get_device() != dev or v_scales.get_device() != dev \
+                or block_table.get_device() != dev or lens.get_device() != dev:
+            raise AttnError("the cache's tensors must be on one CUDA device")
+        if not (k_codes.is_contiguous() and v_codes.is_contiguous() and k_scales.is_contiguous()
+                and v_scales.is_contiguous() and block_table.is_contiguous() and lens.is_contiguous()):
+            raise AttnError("the cache's tensors must be contiguous")
+    except AttributeError as e:
+        raise AttnError(f"the cache, its tables and {lens_name} must be tensors") from e
+    P, page_size, Hkv, D = shape
+    return (KV_E4M3 if kind is _U8 else KV_INT8), P, page_size, Hkv, D, page_size // sshape[1], dev
+
+
+@functools.lru_cache(maxsize=256)
+def _decode_q8_need(Hq, Hkv, D):
+    return int(load_library().attn_decode_paged_q8_workspace_bytes(Hq, Hkv, D))
 
 
 def _q8_buffer(t, dtype, shape, dev, name):
     """Checks one tensor of a call: type, exact shape, device, contiguity."""
     if not isinstance(t, torch.Tensor) or t.dtype is not dtype or t.shape != shape:
         raise AttnError(f"{name}: expected a {dtype} tensor of shape {tuple(shape)}")
-    if not t.is_cuda or t.get_device() != dev or not t.is_contiguous():
+    if t.get_device() != dev or not t.is_contiguous():
         raise AttnError(f"{name}: expected a contiguous CUDA tensor on the cache's device")
 
 
@@ -551,8 +557,7 @@ def decode_paged_q8(q, k_codes, v_codes, k_scales, v_scales, block_table, seq_le
         _q8_buffer(out, _BF16, (N, Hq, D), dev, "out")
     if lse is not None:
         _q8_buffer(lse, _F32, (N, Hq), dev, "lse")
-    lib = load_library()
-    need = lib.attn_decode_paged_q8_workspace_bytes(Hq, Hkv, D)
+    need = _decode_q8_need(Hq, Hkv, D)
     if need == 0:
         raise AttnError("invalid decode configuration", 1)
     status = _q8_scratch(workspace, need, device_status, dev)
@@ -566,7 +571,7 @@ def decode_paged_q8(q, k_codes, v_codes, k_scales, v_scales, block_table, seq_le
         lse = q.new_empty((N, Hq), dtype=_F32)
     if workspace is None:
         workspace = q.new_empty(need, dtype=_U8)
-    st = lib.attn_decode_paged_q8(
+    st = load_library().attn_decode_paged_q8(
         q.data_ptr(), k_codes.data_ptr(), v_codes.data_ptr(), k_scales.data_ptr(), v_scales.data_ptr(),
         block_table.data_ptr(), seq_lens.data_ptr(), fmt, N, Hq, Hkv, D, page_size, block, max_pages, P,
         default_scale(D) if scale is None else scale, o.data_ptr(), None if lse is None else lse.data_ptr(),

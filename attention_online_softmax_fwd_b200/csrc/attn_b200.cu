@@ -585,6 +585,7 @@ int launch_decode_q8(const CUtensorMap& tk, const CUtensorMap& tv, DecodeQ8Param
   const unsigned grid = unsigned(p.teams * p.team);
   decode_q8_kernel<D, NH, GP, I8><<<dim3(grid), dim3(kQ8Threads), L::kDynamic, stream>>>(tk, tv, p);
   if (int st = launch_status()) return st;
+  if (p.whole) return ATTN_OK;   // no sequence is cut
   cudaLaunchAttribute attr[1];   // scheduled while the last CTAs run; waits for them before it reads
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
@@ -1199,6 +1200,7 @@ int attn_decode_paged_q8(const void* q, const void* k_codes, const void* v_codes
   p.groups = (p.rows128 + p.team - 1) / p.team;
   // the kernel counts the batch's tiles in 32 bits (2^30 of them are 140 thousand million tokens)
   const long long tiles = ((long long)max_pages_per_seq * page_size + kQ8Tok - 1) / kQ8Tok;
+  p.whole = tiles <= 4 ? 1 : 0;
   if (tiles > (1ll << 30) / p.groups / num_seqs) return ATTN_ERR_UNSUPPORTED;
   p.part_rows = L.part_rows;
   p.scale_log2 = scale * 1.4426950408889634f;

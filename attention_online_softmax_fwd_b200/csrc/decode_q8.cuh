@@ -31,7 +31,10 @@
 // 128-byte rows are thus read at about the same time: with each CTA on its own work
 // the same copies reach 5.0 to 5.5 TB/s instead of 6.5. A sequence that lies inside a
 // run is written at once; the parts of one that is cut are merged by
-// decode_q8_merge_kernel, and each CTA has two at most, whatever the lengths.
+// decode_q8_merge_kernel, and each CTA has two at most, whatever the lengths. Where
+// the block tables hold at most 512 tokens a sequence the runs are of whole sequences:
+// nothing is cut, and the merge (2.3 us or more on the GPU, 2.5 on the host) is not
+// launched.
 //
 // A CTA has two softmax warpgroups (one token of a tile per thread), two producer warps
 // (one walks the lengths and block tables, copies K by TMA and the scales by
@@ -46,7 +49,7 @@
 // at a time. The four warps of a warpgroup exchange the tile's maxima of y once, so
 // that its 128 tokens share one reference and P V is one accumulation. (Without the
 // exchange, each warp keeping a reference and accumulators of its own, O took four
-// times the registers and tensor-memory reads: 92 us instead of XX for 16 sequences
+// times the registers and tensor-memory reads: 92 us instead of 73 for 16 sequences
 // of 8192 tokens with 8 query heads a group.) O stays in fp32 registers (thread =
 // head dimension) and is rescaled there when Y grows, which is why TMEM holds only
 // the tile's own products. When the CTA's part of the sequence ends, the warpgroup
@@ -87,6 +90,7 @@ struct DecodeQ8Params {
   int box;                     // tokens per TMA copy
   int rows128;                 // 128-byte rows of a token that items are made of (solo: one per KV head)
   int solo;                    // D = 64, one head of a row at a time
+  int whole;                   // runs of whole sequences: none is cut
   int team, groups, teams;     // lanes of a team, ceil(rows128 / team), teams
   int part_rows;               // query rows of a part: G, or 2 G for two heads
   float scale_log2;            // softmax scale * log2(e), without the K scale
@@ -294,8 +298,8 @@ __device__ __forceinline__ float join_digits(uint32_t hi, uint32_t lo) {
   else return fmaf(__uint_as_float(lo), 0.0625f, __uint_as_float(hi));
 }
 
-// Tiles of a sequence of (clamped) length `len`.
-__device__ __forceinline__ int q8_tiles(int len) { return (len + kQ8Tok - 1) / kQ8Tok; }
+// Units of work of a sequence of (clamped) length `len`: its tiles, or one for all of it.
+__device__ __forceinline__ int q8_units(int len, int whole) { return whole ? min(len, 1) : (len + kQ8Tok - 1) / kQ8Tok; }
 __device__ __forceinline__ int q8_clamp_len(int len, int capacity) { return len < 0 ? 0 : min(len, capacity); }
 
 template <int D, int NH, int GP, bool I8>
@@ -377,7 +381,7 @@ __global__ void __launch_bounds__(kQ8Threads, DecodeQ8Smem<D, NH, GP, I8>::kBloc
     for (int i = scan_at; i < scan_end; i += 4) {
       const int len = i == scan_at ? first_len : __ldg(&p.seq_lens[i]);
       if (blockIdx.x == 0 && (len < 0 || len > capacity)) raise_status(p.status, ATTN_ERR_DEVICE_BOUNDS);
-      sum += q8_tiles(q8_clamp_len(len, capacity));
+      sum += q8_units(q8_clamp_len(len, capacity), p.whole);
     }
     sum += __shfl_xor_sync(0xffffffffu, sum, 1);
     sum += __shfl_xor_sync(0xffffffffu, sum, 2);
@@ -416,7 +420,7 @@ __global__ void __launch_bounds__(kQ8Threads, DecodeQ8Smem<D, NH, GP, I8>::kBloc
     const int per_group = __shfl_sync(0xffffffffu, incl, 31);
     const int total = per_group * p.groups;
     // at least two tiles for each team (so no team without one between two parts): a cut costs as much as a tile
-    const int teams = min((total + 1) / 2, p.teams);
+    const int teams = min(p.whole ? total : (total + 1) / 2, p.teams);
     const int quot = teams > 0 ? total / teams : 0, extra = total - quot * teams;   // the first `extra` have one more
     const bool work = team < teams;
     const int begin = work ? team * quot + min(team, extra) : 0;
@@ -443,7 +447,7 @@ __global__ void __launch_bounds__(kQ8Threads, DecodeQ8Smem<D, NH, GP, I8>::kBloc
       int t = 2 * l0;
       if (x >= scan[t]) x -= scan[t++];
       seq = t * per_entry;
-      for (int tiles; x >= (tiles = q8_tiles(len_at(seq))); ++seq) x -= tiles;
+      for (int units; x >= (units = q8_units(len_at(seq), p.whole)); ++seq) x -= units;
       a = x;
     }
     auto page_of = [&](int s, int t0) -> int {   // physical page of chunk c of the tile at t0
@@ -473,7 +477,7 @@ __global__ void __launch_bounds__(kQ8Threads, DecodeQ8Smem<D, NH, GP, I8>::kBloc
           for (;;) {
             if (seq == p.num_seqs) { seq = 0; ++grp; }
             len = len_at(seq);
-            tiles = q8_tiles(len);
+            tiles = q8_units(len, p.whole);
             if (tiles > a) break;
             ++seq;
             a = 0;
@@ -481,7 +485,7 @@ __global__ void __launch_bounds__(kQ8Threads, DecodeQ8Smem<D, NH, GP, I8>::kBloc
           nx.seq = seq; nx.grp = grp; nx.tiles = tiles; nx.pos = pos;
           nx.n = min(tiles - a, end - pos);
           nx.t_begin = a * kQ8Tok;
-          nx.t_end = min((a + nx.n) * kQ8Tok, len);
+          nx.t_end = p.whole ? len : min((a + nx.n) * kQ8Tok, len);
           nx_page = page_of(seq, nx.t_begin);
           pos += nx.n;
           a += nx.n;
@@ -538,7 +542,7 @@ __global__ void __launch_bounds__(kQ8Threads, DecodeQ8Smem<D, NH, GP, I8>::kBloc
         ti.bad = int(~good_mask & 0xFFu);
         // 1: first tile of the part; 2: last; 8: its warpgroup's last of the part; 16: the part has several
         ti.flags = (first ? 1 : 0) | (t0 + kQ8Tok >= w.t_end ? 2 : 0) | (t0 + 2 * kQ8Tok >= w.t_end ? 8 : 0) |
-                   (w.n > 1 ? 16 : 0);
+                   (w.t_end - w.t_begin > kQ8Tok ? 16 : 0);
         ti.len = part_no;
         info[slot] = ti;
         const uint32_t qbytes = first ? uint32_t(q_rows * D * 2) : 0u;
@@ -561,7 +565,7 @@ __global__ void __launch_bounds__(kQ8Threads, DecodeQ8Smem<D, NH, GP, I8>::kBloc
       t0 += kQ8Tok;
       fetch = first;
     }
-    if (lane == 0) p.ws_cut[blockIdx.x] = cut;
+    if (lane == 0 && !p.whole) p.ws_cut[blockIdx.x] = cut;
     for (int i = 0; i < 2 && ok; ++i) {   // end-of-work markers, one for each warpgroup: stages with no copies
       ok = __all_sync(0xffffffffu, q8_wait(&empty[slot], phase ^ 1u, abort_flag, p.status));
       if (!ok) break;
@@ -585,6 +589,13 @@ __global__ void __launch_bounds__(kQ8Threads, DecodeQ8Smem<D, NH, GP, I8>::kBloc
   } else if (warp == kQ8VWarp) {
     // ------------------------------------------------------------ producer warp: V, as the first one says
     setmaxnreg_dec<L::kHelperRegs>();
+    for (int s = blockIdx.x; s < p.num_seqs; s += gridDim.x) {   // sequences without tokens
+      if (__ldg(&p.seq_lens[s]) > 0) continue;
+      uint4* rows = reinterpret_cast<uint4*>(p.o + size_t(s) * p.Hq * D);
+      for (int i = lane; i < p.Hq * (D / 8); i += 32) rows[i] = make_uint4(0, 0, 0, 0);
+      if (p.lse)
+        for (int h = lane; h < p.Hq; h += 32) p.lse[size_t(s) * p.Hq + h] = -__int_as_float(0x7f800000);
+    }
     int slot = 0;
     uint32_t phase = 0;
     while (__all_sync(0xffffffffu, q8_wait(&v_go[slot], phase, abort_flag, p.status))) {
@@ -968,21 +979,15 @@ __global__ void __launch_bounds__(kQ8Threads, DecodeQ8Smem<D, NH, GP, I8>::kBloc
 
 // The cut sequences: CTA (i, r) merges query row r of the sequence whose first part split CTA i
 // holds, if it holds one; its other parts are the first ones of the same lane in the following
-// teams. Sequences without tokens are written here too (o = 0, lse = -inf).
+// teams. (Merged instead by the decode CTA that finishes the last part, found with a counter in
+// the workspace, a call saves this launch but took longer: 39 us against 21 for one sequence of
+// 32768 tokens, 117 against 102 for a batch of 64, since one warpgroup then walks all parts.)
 template <int D>
 __global__ void __launch_bounds__(D) decode_q8_merge_kernel(const DecodeQ8Params p) {
   __shared__ float weight[kQ8MaxCtas], warp_max[D / 32];
   const float neg_inf = -__int_as_float(0x7f800000);
   const int d = threadIdx.x;
   grid_dependency_wait();
-  if (blockIdx.y == 0) {
-    for (int s = blockIdx.x; s < p.num_seqs; s += gridDim.x) {
-      if (__ldg(&p.seq_lens[s]) > 0) continue;
-      for (int h = 0; h < p.Hq; ++h) p.o[(size_t(s) * p.Hq + h) * D + d] = __float2bfloat16_rn(0.f);
-      if (p.lse)
-        for (int h = d; h < p.Hq; h += D) p.lse[size_t(s) * p.Hq + h] = neg_inf;
-    }
-  }
   const int4 cut = p.ws_cut[blockIdx.x];
   if (cut.x < 0) return;
   const int first = int(blockIdx.x) / p.team, lane = int(blockIdx.x) % p.team;

@@ -222,6 +222,29 @@ def test_decode(cuda_device, kind, Hq, Hkv, D, page, block):
 
 
 @pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("N,Hq,Hkv,D,cap", [(11, 8, 2, 128, 512), (700, 4, 2, 64, 512), (700, 4, 2, 64, 640),
+                                            (333, 3, 3, 128, 160), (40, 26, 13, 128, 768), (70, 22, 22, 64, 528)])
+def test_decode_many_short_sequences(cuda_device, kind, N, Hq, Hkv, D, cap):
+    """Batches of many sequences (more than the 64 sums and the 32-wide window of the work walk), tables of at
+    most 512 tokens (whole sequences a CTA) and of more (runs of tiles), head counts that do not divide a team."""
+    g = torch.Generator().manual_seed(6450 + N + cap)
+    lens = torch.randint(0, cap + 1, (N,), generator=g)
+    lens[torch.randperm(N, generator=g)[:N // 5]] = 0
+    lens[torch.randperm(N, generator=g)[:4]] = torch.tensor([cap, 1, 128, 129])
+    lens = lens.tolist()
+    cache = gen.paged_decode_inputs(N, Hq, Hkv, D, 16, 0, 0, seed=6451, lens=lens, max_pages=cap // 16, poison=False)
+    codes = quantized(cache, 16, kind)
+    scale = gen.attn_scale(D)
+    o_ref, lse_ref = orc.decode_paged_q8(cache.q, *codes[:2], *codes[2:], cache.block_table, cache.seq_lens, scale)
+    o_ref, lse_ref = empty_rows(o_ref, lse_ref, lens)
+    st = torch.zeros(1, dtype=torch.int32, device=cuda_device)
+    o, lse = ab.decode_paged_q8(*to(cuda_device, cache.q, *codes, cache.block_table, cache.seq_lens), scale=scale,
+                                device_status=st)
+    assert int(st) == 0
+    compare_output(o, o_ref, lse, lse_ref, label=f"{kind} N={N}")
+
+
+@pytest.mark.parametrize("kind", KINDS)
 def test_decode_full_size(cuda_device, kind):
     """64 sequences, lengths uniform in [512, 8192], Hq=32, Hkv=8, D=128, page 16, one scale per 16 tokens."""
     c = gen.CONFIGS["paged_gqa_decode"]
