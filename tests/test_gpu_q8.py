@@ -347,6 +347,62 @@ def test_decode_bad_pages_and_lengths(cuda_device):
     assert (o[2:] == 0).all() and torch.isneginf(lse[2:]).all()
 
 
+def test_decode_nan_codes_stay_with_their_head(cuda_device):
+    """Two heads of D = 64 share a 128-byte row of a tile: an E4M3 NaN code of one head's key or value must not
+    reach the other's outputs."""
+    lens = [200, 90, 300]
+    cache = gen.paged_decode_inputs(len(lens), 8, 4, 64, 16, 0, 0, seed=6550, lens=lens, poison=False)
+    kc, vc, ks, vs = quantized(cache, 16, "e4m3")
+    scale = gen.attn_scale(64)
+    o_ref, lse_ref = orc.decode_paged_q8(cache.q, kc, vc, ks, vs, cache.block_table, cache.seq_lens, scale)
+    kc[cache.block_table[0, 3].long(), 5, 1, 7] = 0x7F        # a key of head 1
+    vc[cache.block_table[2, 2].long(), 9, 2, 11] = 0xFF       # one dimension of a value of head 2
+    o, lse = ab.decode_paged_q8(*to(cuda_device, cache.q, kc, vc, ks, vs, cache.block_table, cache.seq_lens), scale=scale)
+    o = o.float().cpu().numpy()
+    bad = np.zeros(o.shape, bool)
+    bad[0, 2:4] = True
+    bad[2, 4:6, 11] = True
+    assert np.isnan(o[bad]).all()
+    compare_output(o, np.where(bad, 0.0, o_ref), mask=~bad)
+    ok = ~bad.all(-1)
+    assert np.abs(lse.cpu().numpy()[ok] - lse_ref[ok]).max() <= 1e-3
+
+
+@pytest.mark.parametrize("kind", KINDS)
+def test_pages_beyond_four_gigabytes(cuda_device, kind):
+    """Append, read back and decode on pages whose codes lie past 2^32 bytes of the pool."""
+    g = torch.Generator().manual_seed(6560)
+    page, block, Hkv, D, T = 256, 32, 8, 128, 300
+    P = 17000                                             # 4.46e9 codes in each pool
+    dt = torch.uint8 if kind == "e4m3" else torch.int8
+    kc = torch.zeros(P, page, Hkv, D, dtype=dt, device=cuda_device)
+    vc = torch.zeros_like(kc)
+    ks = torch.ones(P, page // block, Hkv, device=cuda_device)
+    vs = torch.ones_like(ks)
+    bt = torch.tensor([[P - 1, P - 3], [16500, 2]], dtype=torch.int32, device=cuda_device)
+    kn, vn = [torch.randn(2, T, Hkv, D, generator=g).to(torch.bfloat16) for _ in range(2)]
+    st = torch.zeros(1, dtype=torch.int32, device=cuda_device)
+    ab.kv_append_q8(*to(cuda_device, kn, vn), kc, vc, ks, vs, bt, torch.zeros(2, dtype=torch.int32, device=cuda_device),
+                    device_status=st)
+    # the oracle sees the four pages alone
+    ids = bt.flatten().long()
+    small = torch.arange(4, dtype=torch.int32).view(2, 2)
+    z = np.zeros((4, page, Hkv, D), np.uint8 if kind == "e4m3" else np.int8)
+    one = np.ones((4, page // block, Hkv))
+    ref = orc.kv_append_q8(z, z, one, one, small, np.zeros(2, int), kn, vn)
+    for got, want in zip((kc, vc, ks, vs), ref):
+        assert np.array_equal(got[ids].cpu().numpy(), want.astype(got[ids].cpu().numpy().dtype))
+    sl = torch.tensor([T, T], dtype=torch.int32, device=cuda_device)
+    k, v = ab.kv_read_q8(kc, vc, ks, vs, bt, sl, num_tokens=T, device_status=st)
+    pool = orc.q8_dequant(ref[0], ref[2]).reshape(2, 2 * page, Hkv, D)[:, :T]
+    assert np.array_equal(k.double().cpu().numpy(), pool)
+    q = torch.randn(2, 32, D, generator=g).to(torch.bfloat16)
+    o, lse = ab.decode_paged_q8(q.to(cuda_device), kc, vc, ks, vs, bt, sl, device_status=st)
+    o_ref, l_ref = orc.decode_paged_q8(q, *ref, small, sl.cpu(), gen.attn_scale(D))
+    compare_output(o, o_ref, lse, l_ref, label=f"far pages {kind}")
+    assert int(st) == 0
+
+
 # ------------------------------------------------------------------ prefill, and the loop of them
 
 @pytest.mark.parametrize("kind", KINDS)
@@ -367,6 +423,29 @@ def test_prefill(cuda_device, kind, Hq, Hkv, D, page, block, Sq):
     compare_output(o, o_ref, lse, lse_ref, label=f"prefill {kind}")
     o2, lse2 = ab.prefill_paged_q8(*args, scale=scale)
     assert torch.equal(o, o2) and torch.equal(lse, lse2)
+
+
+def test_prefill_bad_pages_and_lengths(cuda_device):
+    """As the bf16 chunked prefill: keys of a page outside the pool read as zeros, a length outside
+    [Sq, capacity] is clamped, both reported; the other sequences are untouched."""
+    Sq, lens = 40, [100, 90, 64]
+    c = gen.paged_prefill_inputs(3, Sq, 4, 2, 64, 16, lens, seed=6650, poison=False)
+    kc, vc, ks, vs = quantized(c, 16, "int8")
+    scale = gen.attn_scale(64)
+    bt, sl = c.block_table.clone(), c.seq_lens.clone()
+    bad_page = int(bt[0, 1])
+    bt[0, 1] = 10 ** 7
+    sl[1] = 10 ** 6                       # clamped to the table's capacity: 112 tokens
+    st = torch.zeros(1, dtype=torch.int32, device=cuda_device)
+    o, lse = ab.prefill_paged_q8(*to(cuda_device, c.q, kc, vc, ks, vs, bt, sl), scale=scale, device_status=st)
+    assert int(st) == 4
+    zk, zv = kc.clone(), vc.clone()
+    zk[bad_page], zv[bad_page] = 0, 0
+    o_ref, l_ref = orc.prefill_paged_q8(c.q, zk, zv, ks, vs, c.block_table, c.seq_lens, scale, seqs=[0, 2])
+    for b in (0, 2):
+        compare_output(o[b], o_ref[b], lse[b], l_ref[b], label=f"sequence {b}")
+    o1, _ = ab.prefill_paged_q8(*to(cuda_device, c.q[2:].contiguous(), kc, vc, ks, vs, bt[2:], sl[2:]), scale=scale)
+    assert torch.equal(o1[0], o[2])
 
 
 @pytest.mark.parametrize("kind", KINDS)
