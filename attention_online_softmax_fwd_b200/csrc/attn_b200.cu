@@ -591,7 +591,7 @@ int launch_decode_q8(const CUtensorMap& tk, const CUtensorMap& tv, DecodeQ8Param
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(grid, unsigned(p.part_rows));
-  cfg.blockDim = dim3(D);
+  cfg.blockDim = dim3(128);
   cfg.stream = stream;
   cfg.attrs = attr;
   cfg.numAttrs = 1;

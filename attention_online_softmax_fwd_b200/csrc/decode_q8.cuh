@@ -977,65 +977,98 @@ __global__ void __launch_bounds__(kQ8Threads, DecodeQ8Smem<D, NH, GP, I8>::kBloc
   if (warp == kQ8ScoreWarp) tmem_dealloc(tmem, L::kTmemCols);
 }
 
-// The cut sequences: CTA (i, r) merges query row r of the sequence whose first part split CTA i
-// holds, if it holds one; its other parts are the first ones of the same lane in the following
-// teams. (Merged instead by the decode CTA that finishes the last part, found with a counter in
-// the workspace, a call saves this launch but took longer: 39 us against 21 for one sequence of
-// 32768 tokens, 117 against 102 for a batch of 64, since one warpgroup then walks all parts.)
+// The cut sequences: CTA (i, r) merges query row r of the one whose first part decode CTA i holds, if
+// it holds one; its other parts are the first ones of the same lane in the following teams. Bound by
+// latency (its loads are a few KB a CTA, out of L2), so a CTA's four warps take sixteen parts each at a
+// time, all sixteen in flight, a lane D / 32 neighbouring dimensions, and a sequence of at most sixteen
+// parts ends in warp 0 without an exchange. One thread a dimension over all parts, eight in flight, made
+// a call of one sequence of 32768 tokens 19.5 us long with 8 KV heads (37 parts; 18.5 so) and 17.1 with
+// one (148 parts; 13.8 so); a warp a row over all parts 21.9 with 8 KV heads. Merged instead by the
+// decode CTA that finishes the last part, found with a counter in the workspace, a call saves this
+// launch but took longer (39 us against 21 when it was tried, and 117 against 102 for 64 sequences): a
+// fence and two dependent loads take microseconds while the other CTAs stream.
 template <int D>
-__global__ void __launch_bounds__(D) decode_q8_merge_kernel(const DecodeQ8Params p) {
-  __shared__ float weight[kQ8MaxCtas], warp_max[D / 32];
+__global__ void __launch_bounds__(128) decode_q8_merge_kernel(const DecodeQ8Params p) {
+  constexpr int E = D / 32;
+  __shared__ float sh_m[4], sh_sum[4];
+  __shared__ __align__(16) float sh_acc[4][D];
   const float neg_inf = -__int_as_float(0x7f800000);
-  const int d = threadIdx.x;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   grid_dependency_wait();
   const int4 cut = p.ws_cut[blockIdx.x];
   if (cut.x < 0) return;
-  const int first = int(blockIdx.x) / p.team, lane = int(blockIdx.x) % p.team;
-  const int row = cut.y * p.team + lane, r = blockIdx.y;
+  const int first = int(blockIdx.x) / p.team, team_lane = int(blockIdx.x) % p.team;
+  const int row = cut.y * p.team + team_lane, r = int(blockIdx.y);
   const int nh = p.part_rows > p.G && r >= p.G ? 1 : 0;
   const int head = (p.part_rows > p.G ? row * 2 : row) + nh;
-  if (head >= p.Hkv) return;
-  const int n = cut.z - first + 1;         // parts: at most one per team
+  if (r >= p.part_rows || head >= p.Hkv) return;
+  const int n = cut.z - first + 1;                         // parts: at most one per team
   auto part_row = [&](int i) {
-    const int cta = (first + i) * p.team + lane;
-    return size_t(cta * 2 + (i == 0 ? cut.w : 0)) * p.part_rows + r;
+    return size_t(((first + i) * p.team + team_lane) * 2 + (i == 0 ? cut.w : 0)) * p.part_rows + r;
   };
-  // thread i holds the log2-sum-exp of parts i, i + D, ...: all of them in flight at once
-  float mine[(kQ8MaxCtas + D - 1) / D];
-  float m = neg_inf;
+  float m = neg_inf, sum = 0.f, acc[E];
 #pragma unroll
-  for (int k = 0; k < (kQ8MaxCtas + D - 1) / D; ++k) {
-    mine[k] = k * D + d < n ? p.ws_lse[part_row(k * D + d)] : neg_inf;
-    m = max_nan(m, mine[k]);
-  }
-  m = warp_max_nan(m);
-  if ((d & 31) == 0) warp_max[d >> 5] = m;
-  __syncthreads();
+  for (int e = 0; e < E; ++e) acc[e] = 0.f;
+  for (int i0 = warp * 16; i0 < n; i0 += 64) {   // lanes 0..15: the weights of parts i0 + lane
+    const int k1 = min(16, n - i0);
+    const float lse = lane < k1 ? p.ws_lse[part_row(i0 + lane)] : neg_inf;
+    const float mx = max_nan(m, warp_max_nan(lse)), off = mx == neg_inf ? 0.f : mx;
+    const float old = fast_exp2(m - off), w = fast_exp2(lse - off);
+    m = mx;
+    sum = fmaf(sum, old, w);                     // this lane's part of the sum
 #pragma unroll
-  for (int k = 0; k < D / 32; ++k) m = max_nan(m, warp_max[k]);
-  const float off = m == neg_inf ? 0.f : m;
+    for (int e = 0; e < E; ++e) acc[e] *= old;
+    float v[16][E];
 #pragma unroll
-  for (int k = 0; k < (kQ8MaxCtas + D - 1) / D; ++k)
-    if (k * D + d < n) weight[k * D + d] = fast_exp2(mine[k] - off);
-  __syncthreads();
-  float sum = 0.f, acc = 0.f;
-  const float* src = p.ws_o + part_row(0) * D + d;
-  const size_t step = size_t(p.team) * 2 * p.part_rows * D;       // parts 1, 2, ...: slot 0 of the next teams
-  const float* rest = p.ws_o + (part_row(0) - size_t(cut.w) * p.part_rows) * D + d;
-  for (int i0 = 0; i0 < n; i0 += 8) {
-    float v[8];
+    for (int k = 0; k < 16; ++k) {
+      const float* src = p.ws_o + part_row(min(i0 + k, n - 1)) * D + lane * E;
+      if constexpr (E == 4) {
+        const float4 t = *reinterpret_cast<const float4*>(src);
+        v[k][0] = t.x; v[k][1] = t.y; v[k][2] = t.z; v[k][3] = t.w;
+      } else {
+        const float2 t = *reinterpret_cast<const float2*>(src);
+        v[k][0] = t.x; v[k][1] = t.y;
+      }
+    }
 #pragma unroll
-    for (int k = 0; k < 8; ++k) v[k] = i0 + k < n ? (i0 + k == 0 ? *src : rest[(i0 + k) * step]) : 0.f;
+    for (int k = 0; k < 16; ++k) {
+      const float wk = __shfl_sync(0xffffffffu, w, k);
 #pragma unroll
-    for (int k = 0; k < 8; ++k) {
-      const float wt = i0 + k < n ? weight[i0 + k] : 0.f;
-      sum += wt;
-      acc = fmaf(wt, v[k], acc);
+      for (int e = 0; e < E; ++e) acc[e] = fmaf(k < k1 ? wk : 0.f, v[k][e], acc[e]);
     }
   }
+#pragma unroll
+  for (int d = 16; d > 0; d >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
+  if (n > 16) {                                  // else warp 0 holds it all
+    if (lane == 0) { sh_m[warp] = m; sh_sum[warp] = sum; }
+#pragma unroll
+    for (int e = 0; e < E; ++e) sh_acc[warp][lane * E + e] = acc[e];
+    __syncthreads();
+    if (warp != 0) return;
+#pragma unroll
+    for (int w = 0; w < 4; ++w) m = w == 0 ? sh_m[0] : max_nan(m, sh_m[w]);
+    const float off = m == neg_inf ? 0.f : m;
+    sum = 0.f;
+#pragma unroll
+    for (int e = 0; e < E; ++e) acc[e] = 0.f;
+#pragma unroll
+    for (int w = 0; w < 4; ++w) {                  // the four warps' shares onto one maximum
+      const float f = fast_exp2(sh_m[w] - off);
+      sum = fmaf(f, sh_sum[w], sum);
+#pragma unroll
+      for (int e = 0; e < E; ++e) acc[e] = fmaf(f, sh_acc[w][lane * E + e], acc[e]);
+    }
+  } else if (warp != 0) {
+    return;
+  }
   const size_t at = size_t(cut.x) * p.Hq + size_t(head) * p.G + (r - nh * p.G);
-  p.o[at * D + d] = __float2bfloat16_rn(sum == 0.f ? 0.f : acc / sum);
-  if (p.lse && d == 0) p.lse[at] = sum == 0.f ? neg_inf : (m + __log2f(sum)) * 0.69314718055994531f;
+  const float inv = sum == 0.f ? 0.f : 1.f / sum;
+  uint32_t out[E / 2];
+#pragma unroll
+  for (int e = 0; e < E / 2; ++e) out[e] = pack_bf16x2(acc[2 * e] * inv, acc[2 * e + 1] * inv);
+  if constexpr (E == 4) *reinterpret_cast<uint2*>(p.o + at * D + lane * E) = make_uint2(out[0], out[1]);
+  else *reinterpret_cast<uint32_t*>(p.o + at * D + lane * E) = out[0];
+  if (p.lse && lane == 0) p.lse[at] = sum == 0.f ? neg_inf : (m + __log2f(sum)) * 0.69314718055994531f;
 }
 
 }  // namespace attn
