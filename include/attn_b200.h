@@ -414,7 +414,9 @@ int attn_decode_paged_q8(const void* q, const void* k_codes, const void* v_codes
  * attn_prefill_paged; the workspace (16-byte aligned, contents ignored) holds at
  * least attn_prefill_paged_q8_workspace_bytes(...) bytes: bf16 K and V of
  * B * max_pages_per_seq pages, so a table trimmed to the pages in use keeps it
- * small. Returns 0 for invalid arguments or an overflowing size.
+ * small. Returns 0 for invalid arguments or an overflowing size. A key or value
+ * that reads as NaN or infinity makes o and the LSE of the queries that see it NaN
+ * (all dimensions) and no others.
  */
 size_t attn_prefill_paged_q8_workspace_bytes(int B, int Hkv, int D, int max_pages_per_seq, int page_size);
 int attn_prefill_paged_q8(const void* q, const void* k_codes, const void* v_codes, const float* k_scales,

@@ -425,6 +425,39 @@ def test_prefill(cuda_device, kind, Hq, Hkv, D, page, block, Sq):
     assert torch.equal(o, o2) and torch.equal(lse, lse2)
 
 
+@pytest.mark.parametrize("kind", KINDS)
+def test_prefill_nan_reaches_only_the_queries_that_see_it(cuda_device, kind):
+    """NaN scales (and E4M3 NaN codes) of keys and values inside the chunk, hidden from its earlier queries by
+    the causal mask but in their key tiles: those queries are untouched, the later ones NaN."""
+    Sq, lens, block = 120, [120, 300, 250, 131], 16
+    c = gen.paged_prefill_inputs(4, Sq, 4, 2, 128, 16, lens, seed=6640, poison=False)
+    kc, vc, ks, vs = quantized(c, block, kind)
+    scale = gen.attn_scale(128)
+    o_ref, lse_ref = orc.prefill_paged_q8(c.q, kc, vc, ks, vs, c.block_table, c.seq_lens, scale)
+    page = lambda b, t: int(c.block_table[b, t // 16])
+    seen_from = [None] * 4                    # (first position that sees it, KV head)
+    vs[page(0, 64), 0, 0] = float("nan")
+    seen_from[0] = (64, 0)
+    ks[page(1, 240), 0, 1] = float("nan")
+    seen_from[1] = (240, 1)
+    if kind == "e4m3":
+        vc[page(2, 203), 203 % 16, 1, 100] = 0x7F
+        seen_from[2] = (203, 1)
+        kc[page(3, 130), 130 % 16, 0, 3] = 0xFF
+        seen_from[3] = (130, 0)
+    o, lse = ab.prefill_paged_q8(*to(cuda_device, c.q, kc, vc, ks, vs, c.block_table, c.seq_lens), scale=scale)
+    bad = np.zeros(o.shape, bool)             # [B, Sq, Hq, D]
+    for b, at in enumerate(seen_from):
+        if at is not None:
+            bad[b, at[0] - (lens[b] - Sq):, at[1] * 2:at[1] * 2 + 2] = True
+    o, lse = o.float().cpu().numpy(), lse.cpu().numpy()
+    assert np.isnan(o[bad]).all()
+    compare_output(o, np.where(bad, 0.0, o_ref), mask=~bad)
+    row_bad = bad.any(-1).transpose(0, 2, 1)
+    assert np.isnan(lse[row_bad]).all()
+    assert np.abs(lse[~row_bad] - lse_ref[~row_bad]).max() <= 1e-3
+
+
 def test_prefill_bad_pages_and_lengths(cuda_device):
     """As the bf16 chunked prefill: keys of a page outside the pool read as zeros, a length outside
     [Sq, capacity] is clamped, both reported; the other sequences are untouched."""
