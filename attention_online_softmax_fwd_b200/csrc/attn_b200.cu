@@ -148,19 +148,34 @@ int encode_bshd(CUtensorMap* map, const void* base, int B, int S, int H, int D, 
 
 int launch_status() { return cudaGetLastError() == cudaSuccess ? ATTN_OK : ATTN_ERR_CUDA; }
 
-template <int D, bool CAUSAL, bool SKIP, bool PAGED = false, bool DBG = false, bool CONTIG = false>
+template <int D, bool CAUSAL, bool SKIP, bool PAGED = false, bool DBG = false, bool CONTIG = false,
+          bool CUT = false>
 int launch_prefill(const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv, const CUtensorMap& tvh,
                    const PrefillParams& p, int sms, cudaStream_t stream) {
-  auto kernel = prefill_kernel<D, CAUSAL, SKIP, PAGED, DBG, CONTIG>;
+  auto kernel = prefill_kernel<D, CAUSAL, SKIP, PAGED, DBG, CONTIG, CUT>;
   constexpr int smem = PrefillSmem<D>::kDynamic;
   // The kernel moves registers between warpgroups with setmaxnreg; the block's
   // launch allocation must cover the split or the increase would never return
   // (checked with the shared-memory limit, once per device).
-  if (int st = set_smem_once<prefill_kernel<D, CAUSAL, SKIP, PAGED, DBG, CONTIG>>(
+  if (int st = set_smem_once<prefill_kernel<D, CAUSAL, SKIP, PAGED, DBG, CONTIG, CUT>>(
           smem, (kPfRegPoolNeeded + kPfThreads - 1) / kPfThreads))
     return st;
   const long long grid = p.num_items < sms ? p.num_items : sms;
-  kernel<<<dim3(unsigned(grid)), dim3(kPfThreads), smem, stream>>>(tq, tk, tv, tvh, p);
+  if constexpr (CONTIG) {   // scheduled while the widening ends; waits for it before it reads
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(unsigned(grid));
+    cfg.blockDim = dim3(kPfThreads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = stream;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    if (cudaLaunchKernelEx(&cfg, kernel, tq, tk, tv, tvh, p) != cudaSuccess) return ATTN_ERR_CUDA;
+  } else {
+    kernel<<<dim3(unsigned(grid)), dim3(kPfThreads), smem, stream>>>(tq, tk, tv, tvh, p);
+  }
   return launch_status();
 }
 
@@ -694,9 +709,11 @@ int check_q8_pool(const void* k_codes, const void* v_codes, const float* k_scale
 }
 
 // Workspace of the prefill over an 8-bit cache: bf16 K and V [num_seqs][max_pages * page_size][Hkv][D],
-// V 256-byte aligned behind K.
+// V 256-byte aligned behind K, then room for the parts of cut items: one a CTA, 256 query rows of fp32 O
+// and LSE (prefill_q8_splits).
+constexpr int kPfQ8MaxCtas = 160;
 struct PrefillQ8Layout {
-  size_t v_off = 0, total = 0;
+  size_t v_off = 0, lse_off = 0, o_off = 0, total = 0;
 };
 bool prefill_q8_layout(int num_seqs, int Hkv, int D, int page_size, int max_pages, PrefillQ8Layout* L) {
   if (num_seqs < 1 || Hkv < 1 || (D != 64 && D != 128) || !valid_page_size(page_size) || max_pages < 1) return false;
@@ -707,8 +724,41 @@ bool prefill_q8_layout(int num_seqs, int Hkv, int D, int page_size, int max_page
   if (!add_size(kv, 255, &v_off)) return false;
   v_off = v_off / 256 * 256;
   if (!add_size(v_off, kv, &end)) return false;
-  L->v_off = v_off; L->total = end;
+  const size_t rows = size_t(kPfQ8MaxCtas) * 2 * kPfRows;
+  if (!add_size(end, 255 + rows * (size_t(D) + 1) * sizeof(float), &L->total)) return false;
+  L->v_off = v_off;
+  L->lse_off = (end + 255) / 256 * 256;
+  L->o_off = L->lse_off + rows * sizeof(float);
+  L->total = L->o_off + rows * size_t(D) * sizeof(float);
   return true;
+}
+
+// Parts that each item's key tiles are cut into: one, unless the items would fill less than half of the SMs
+// and the tables hold more than four tiles of keys.
+int prefill_q8_splits(int items, int sms, long long key_tiles) {
+  const int ctas = sms < kPfQ8MaxCtas ? sms : kPfQ8MaxCtas;
+  if (2ll * items > ctas || key_tiles <= 4) return 1;
+  const long long most = key_tiles < 32 ? key_tiles : 32;   // the merge holds a part a lane
+  return int(ctas / items < most ? ctas / items : most);
+}
+
+// The prefill over the widened cache, and the merge of the parts where items are cut.
+template <int D>
+int launch_prefill_q8(const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv, const PrefillParams& p,
+                      int sms, cudaStream_t stream) {
+  if (p.splits == 1) return launch_prefill<D, true, false, true, false, true>(tq, tk, tv, tv, p, sms, stream);
+  if (int st = launch_prefill<D, true, false, true, false, true, true>(tq, tk, tv, tv, p, sms, stream)) return st;
+  cudaLaunchAttribute attr[1];   // scheduled while the last CTAs run; waits for them before it reads
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(unsigned(((long long)p.B * p.S * p.Hq + 3) / 4));   // at most 160 items of 256 rows
+  cfg.blockDim = dim3(128);
+  cfg.stream = stream;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  if (cudaLaunchKernelEx(&cfg, prefill_merge_kernel<D>, p) != cudaSuccess) return ATTN_ERR_CUDA;
+  return launch_status();
 }
 
 }  // namespace
@@ -1271,6 +1321,10 @@ int attn_prefill_paged_q8(const void* q, const void* k_codes, const void* v_code
   f.n_qblocks = (Sq + 2 * kPfRows - 1) / (2 * kPfRows);
   f.n_qt = (Sq + kPfRows - 1) / kPfRows;
   f.num_items = f.n_qblocks * B * Hq;   // fits, checked above
+  f.splits = prefill_q8_splits(f.num_items, sms, ((long long)p.T + kPfKeys - 1) / kPfKeys);
+  f.num_items *= f.splits;              // no more than the SMs where they are cut
+  f.ws_o = reinterpret_cast<float*>(ws + L.o_off);
+  f.ws_lse = reinterpret_cast<float*>(ws + L.lse_off);
   f.scale_log2 = scale * 1.4426950408889634f;
   f.log2_lambda = -INFINITY;
   f.seq_lens = seq_lens;
@@ -1283,8 +1337,7 @@ int attn_prefill_paged_q8(const void* q, const void* k_codes, const void* v_code
   if (int st = encode_bshd(&tk, p.k_out, B, p.T, Hkv, D)) return st;
   if (int st = encode_bshd(&tv, p.v_out, B, p.T, Hkv, D)) return st;
   if (int st = launch_read_q8(format, D, p, sms, s)) return st;
-  return D == 128 ? launch_prefill<128, true, false, true, false, true>(tq, tk, tv, tv, f, sms, s)
-                  : launch_prefill<64, true, false, true, false, true>(tq, tk, tv, tv, f, sms, s);
+  return D == 128 ? launch_prefill_q8<128>(tq, tk, tv, f, sms, s) : launch_prefill_q8<64>(tq, tk, tv, f, sms, s);
 }
 
 }  // extern "C"

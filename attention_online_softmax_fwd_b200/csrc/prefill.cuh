@@ -54,7 +54,21 @@ struct PrefillParams {
   unsigned long long* skipped_tiles;   // tile skip: count of skipped (query tile, 64-key tile) decisions, or null
   unsigned long long wait_ns;          // pipeline wait limit (kWaitLimitNs unless a test shortens it)
   int withhold_step;                   // test only: the producer leaves out this ring step (-1: none)
+  // CUT: each item's key tiles are cut into up to this many parts, whose outputs go to
+  float* ws_o;                         // [splits][B][S][Hq][D] (normalised) and
+  float* ws_lse;                       // [splits][B][S][Hq] (natural log), for prefill_merge_kernel
+  int splits;
 };
+
+// CUT: part s of the parts of a (sequence, query block) pair whose first query tile visits n0 key tiles:
+// tiles [first, stop) of those each query tile visits; the last part holds all that are left. Empty past the
+// last part. Every part but the last is the same for both query tiles.
+__host__ __device__ __forceinline__ int pf_parts(int splits, int n0) { return splits < n0 ? splits : n0; }
+__host__ __device__ __forceinline__ void pf_part_tiles(int s, int splits, int n0, int& first, int& stop) {
+  const int parts = pf_parts(splits, n0);
+  first = s < parts ? int((long long)s * n0 / parts) : 0x7fffffff;
+  stop = s < parts - 1 ? int((long long)(s + 1) * n0 / parts) : 0x7fffffff;
+}
 
 constexpr int kPfRows = 128;     // rows per query tile
 constexpr int kPfKeys = 128;     // keys per K/V tile (two 64-key decision tiles)
@@ -380,12 +394,16 @@ __device__ __forceinline__ int pf_count_skipped(const PrefillParams& p, int jt, 
 // unpaged prefill), so a tile is D / 64 copies instead of D / 8: the 32 copies of a
 // K/V tile pair from 16-token pages take longer to issue than its products (4 sequences
 // of 2048 new tokens after up to 6144, 32 heads on 8 of D = 128, 8-bit cache: 582 us
-// with the widening, 790 us over 16-token pages of widened keys and values). Here the
-// LSE of a row that sees a NaN is NaN.
+// with the widening, 790 us over 16-token pages of widened keys and values). The LSE of a row that
+// sees a NaN is NaN here.
+// CUT (with CONTIG): each item's key tiles are cut into parts (pf_part_tiles), a CTA
+// each, which prefill_merge_kernel merges: for few items, whose tiles one after another
+// leave most SMs idle.
 // DBG (the test entry point only): the producer's and issuers' wait limit comes
 // from p.wait_ns and the producer leaves out ring step p.withhold_step; every
 // other instantiation waits up to kWaitLimitNs and withholds nothing.
-template <int D, bool CAUSAL, bool SKIP, bool PAGED = false, bool DBG = false, bool CONTIG = false>
+template <int D, bool CAUSAL, bool SKIP, bool PAGED = false, bool DBG = false, bool CONTIG = false,
+          bool CUT = false>
 __global__ void __launch_bounds__(kPfThreads, 1)
     prefill_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
                    const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ CUtensorMap tm_vh,
@@ -459,6 +477,7 @@ __global__ void __launch_bounds__(kPfThreads, 1)
   // Item decode shared by all roles: longest causal blocks first; the G query
   // heads of one KV head are adjacent so their K/V tiles are reused from L2.
   auto item_coords = [&](int item, int& qb, int& b, int& hq) {
+    if constexpr (CUT) item /= p.splits;
     if (ranked) {
       const int pair = pair_order[item / p.Hq];
       b = pair / p.n_qblocks;
@@ -495,6 +514,19 @@ __global__ void __launch_bounds__(kPfThreads, 1)
     return (p.S + kPfKeys - 1) / kPfKeys;
   };
 
+  // CUT: the item's key tiles are those from `first` on, and of a query tile's n tiles count(n) are its
+  // own; every role counts its tiles from there.
+  struct Part {
+    int first, stop;
+    __device__ int count(int n) const { return CUT ? max(0, min(n, stop) - first) : n; }
+  };
+  auto part_of = [&](int item, int qb, int off) {
+    Part part{0, 0x7fffffff};
+    if constexpr (CUT)
+      pf_part_tiles(item % p.splits, p.splits, tile_nkv(qb, 0, tile_rows(qb, 0), off), part.first, part.stop);
+    return part;
+  };
+
   if (ranked) {
     // Rank the pairs by K/V tiles (both query tiles' counts), most first, ties in pair order:
     // with the items in that order the snake gives every CTA about the same work, whatever the
@@ -518,6 +550,8 @@ __global__ void __launch_bounds__(kPfThreads, 1)
     }
     __syncthreads();
   }
+
+  if constexpr (CONTIG) grid_dependency_wait();   // the widened cache
 
   // Register split: warps 0-3 give up registers, the softmax warpgroups take them
   // (kPfRegPoolNeeded is checked against the launch allocation on the host).
@@ -616,11 +650,13 @@ __global__ void __launch_bounds__(kPfThreads, 1)
           const int kvh = hq / (p.Hq / p.Hkv);
           const int off = seq_offset(b, false);
           const int rows0 = tile_rows(qb, 0), rows1 = tile_rows(qb, 1);
-          const int nkv0 = tile_nkv(qb, 0, rows0, off), nkv1 = tile_nkv(qb, 1, rows1, off);
+          const Part part = part_of(item, qb, off);
+          const int nkv0 = part.count(tile_nkv(qb, 0, rows0, off)), nkv1 = part.count(tile_nkv(qb, 1, rows1, off));
           const int n = max(nkv0, nkv1);
+          if (CUT && n == 0) continue;
 #pragma unroll
           for (int x = 0; x < 2; ++x) {
-            if ((x == 0 ? rows0 : rows1) == 0 || !ok) continue;
+            if ((CUT ? (x == 0 ? nkv0 : nkv1) : (x == 0 ? rows0 : rows1)) == 0 || !ok) continue;
             if (!mbar_wait(&bars[L::bQEmpty + x], (qe_bits >> x) & 1u, abort_flag, p.status, wait_lim)) {
               ok = false;
               continue;
@@ -637,7 +673,7 @@ __global__ void __launch_bounds__(kPfThreads, 1)
             bool is_k;
             int tile;
             pf_ring_step<kLead>(step, n, is_k, tile);
-            const int key0 = tile * kPfKeys;
+            const int key0 = (CUT ? part.first + tile : tile) * kPfKeys;
             int halves = 3;   // bit h: 64-key half h of the tile is loaded
             if constexpr (SKIP) {
               if (!is_k) {
@@ -726,8 +762,9 @@ __global__ void __launch_bounds__(kPfThreads, 1)
           item_coords(item, qb, b, hq);
           const int off = seq_offset(b, false);
           const int rows0 = tile_rows(qb, 0), rows1 = tile_rows(qb, 1);
-          const int n = max(tile_nkv(qb, 0, rows0, off), tile_nkv(qb, 1, rows1, off));
-          const int nkv = tile_nkv(qb, x, x == 0 ? rows0 : rows1, off);
+          const Part part = part_of(item, qb, off);
+          const int n = part.count(max(tile_nkv(qb, 0, rows0, off), tile_nkv(qb, 1, rows1, off)));
+          const int nkv = part.count(tile_nkv(qb, x, x == 0 ? rows0 : rows1, off));
           if (nkv > 0) {
             if (!mbar_wait(&bars[L::bQFull + x], qf_ph, abort_flag, p.status, wait_lim)) break;
             qf_ph ^= 1u;
@@ -817,10 +854,11 @@ __global__ void __launch_bounds__(kPfThreads, 1)
       const int off = seq_offset(b, x == 0 && t == 0);
       const int n_keys = PAGED ? off + p.S : p.S;   // keys in the cache (the sequence)
       const int rows = tile_rows(qb, x);
-      const int nkv = tile_nkv(qb, x, rows, off);
+      const Part part = part_of(item, qb, off);
+      const int nkv = part.count(tile_nkv(qb, x, rows, off));
       if (nkv == 0) continue;
       // K/V tiles that both query tiles of the block visit (they alternate on the MUFU there)
-      const int n_common = min(nkv, tile_nkv(qb, 1 - x, tile_rows(qb, 1 - x), off));
+      const int n_common = min(nkv, part.count(tile_nkv(qb, 1 - x, tile_rows(qb, 1 - x), off)));
       const int row0 = qb * 2 * kPfRows + x * kPfRows;
       const int row = row0 + t;
       const bool row_valid = t < rows;
@@ -837,7 +875,7 @@ __global__ void __launch_bounds__(kPfThreads, 1)
         if (!mbar_wait(&bars[L::bSFull + x], sf_ph, no_abort, p.status)) { ok = false; break; }
         sf_ph ^= 1u;
         tc_fence_after();
-        const int key0 = j * kPfKeys;
+        const int key0 = (CUT ? part.first + j : j) * kPfKeys;
         float s[kPfKeys];
         pf_load_scores<CAUSAL>(taddr_s, s, key0, off + row, off + row0, n_keys);
         // S_x is in registers: the tensor pipe may overwrite it with the next tile
@@ -1041,11 +1079,21 @@ __global__ void __launch_bounds__(kPfThreads, 1)
       tc_fence_after();
       const float inv_l = (l.y > 0.f) ? 1.f / l.y : 0.f;
       __nv_bfloat16* orow = p.o + ((size_t(b) * p.S + row) * p.Hq + hq) * D;
+      const size_t part_row = CUT ? ((size_t(item % p.splits) * p.B + b) * p.S + row) * p.Hq + hq : 0;
 #pragma unroll
       for (int c = 0; c < D / 32; ++c) {
         uint32_t r[32];
         ATTN_TMEM_LD32(taddr_o + c * 32, r);
-        if (row_valid) {
+        if constexpr (CUT) {
+          if (row_valid) {
+            float* dst = p.ws_o + part_row * D + c * 32;
+#pragma unroll
+            for (int e = 0; e < 32; e += 4)
+              *reinterpret_cast<float4*>(dst + e) =
+                  make_float4(__uint_as_float(r[e]) * inv_l, __uint_as_float(r[e + 1]) * inv_l,
+                              __uint_as_float(r[e + 2]) * inv_l, __uint_as_float(r[e + 3]) * inv_l);
+          }
+        } else if (row_valid) {
           uint4 w[4];
           uint32_t* wp = reinterpret_cast<uint32_t*>(w);
 #pragma unroll
@@ -1056,9 +1104,10 @@ __global__ void __launch_bounds__(kPfThreads, 1)
           for (int e = 0; e < 4; ++e) dst[e] = w[e];
         }
       }
-      if (row_valid && p.lse)
-        p.lse[(size_t(b) * p.Hq + hq) * p.S + row] =
-            (CONTIG ? l.x != 0.f : l.x > 0.f) ? (m_ref + __log2f(l.x)) * 0.69314718055994531f : neg_inf;
+      float* lse_at = p.lse ? p.lse + (size_t(b) * p.Hq + hq) * p.S + row : nullptr;
+      if constexpr (CUT) lse_at = p.ws_lse + part_row;
+      if (row_valid && lse_at)
+        *lse_at = (CONTIG ? l.x != 0.f : l.x > 0.f) ? (m_ref + __log2f(l.x)) * 0.69314718055994531f : neg_inf;
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive(&bars[L::bOEmpty + x]);
@@ -1070,6 +1119,56 @@ __global__ void __launch_bounds__(kPfThreads, 1)
   __syncthreads();
   tc_fence_after();
   if (warp == kPfIssuerWarp0) tmem_dealloc(tmem, kTmemCols);
+}
+
+// The parts of each query row (CUT) onto one reference: a warp a row, a lane D / 32
+// neighbouring dimensions, the log-sum-exps of up to 32 parts a lane each.
+template <int D>
+__global__ void __launch_bounds__(128) prefill_merge_kernel(const PrefillParams p) {
+  constexpr int E = D / 32;
+  const int lane = threadIdx.x & 31;
+  const long long rows = (long long)p.B * p.S * p.Hq, at = (long long)blockIdx.x * 4 + (threadIdx.x >> 5);
+  const float neg_inf = -__int_as_float(0x7f800000);
+  grid_dependency_wait();
+  if (at >= rows) return;
+  const int hq = int(at % p.Hq), i = int(at / p.Hq % p.S), b = int(at / p.Hq / p.S);
+  const int len = max(p.S, min(__ldg(&p.seq_lens[b]), p.max_pages * p.page_size));
+  const int qrow = i / (2 * kPfRows) * (2 * kPfRows);       // tile A of the row's query block
+  const int n0 = (len - p.S + min(qrow + kPfRows, p.S) - 1) / kPfKeys + 1;
+  const int parts = pf_parts(p.splits, n0);
+  const float lse = lane < parts ? p.ws_lse[(long long)lane * rows + at] : neg_inf;
+  float m = lse;                                            // fmaxf passes a NaN over; it shows in the sum
+#pragma unroll
+  for (int d = 16; d > 0; d >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, d));
+  const float w = fast_exp2((lse - (m == neg_inf ? 0.f : m)) * 1.4426950408889634f);
+  float sum = w, acc[E];
+#pragma unroll
+  for (int d = 16; d > 0; d >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
+#pragma unroll
+  for (int e = 0; e < E; ++e) acc[e] = 0.f;
+#pragma unroll 4
+  for (int s = 0; s < parts; ++s) {
+    const float wt = __shfl_sync(0xffffffffu, w, s);
+    const float* src = p.ws_o + ((long long)s * rows + at) * D + lane * E;
+    float v[E];
+    if constexpr (E == 4) {
+      const float4 t = *reinterpret_cast<const float4*>(src);
+      v[0] = t.x; v[1] = t.y; v[2] = t.z; v[3] = t.w;
+    } else {
+      const float2 t = *reinterpret_cast<const float2*>(src);
+      v[0] = t.x; v[1] = t.y;
+    }
+#pragma unroll
+    for (int e = 0; e < E; ++e) acc[e] = fmaf(wt, v[e], acc[e]);
+  }
+  const float inv = 1.f / sum;                              // every row sees a key: its own
+  uint32_t out[E / 2];
+#pragma unroll
+  for (int e = 0; e < E / 2; ++e) out[e] = pack_bf16x2(acc[2 * e] * inv, acc[2 * e + 1] * inv);
+  if constexpr (E == 4) *reinterpret_cast<uint2*>(p.o + at * D + lane * E) = make_uint2(out[0], out[1]);
+  else *reinterpret_cast<uint32_t*>(p.o + at * D + lane * E) = out[0];
+  if (p.lse && lane == 0)
+    p.lse[((long long)b * p.Hq + hq) * p.S + i] = m + __log2f(sum) * 0.69314718055994531f;
 }
 
 }  // namespace attn

@@ -458,6 +458,31 @@ def test_prefill_nan_reaches_only_the_queries_that_see_it(cuda_device, kind):
     assert np.abs(lse[~row_bad] - lse_ref[~row_bad]).max() <= 1e-3
 
 
+@pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("Hq,Hkv,D,Sq,lens,pages", [
+    (4, 1, 128, 1, [4000, 1, 700], 256), (2, 2, 64, 130, [130, 3100, 257, 1500], 200),
+    (16, 4, 64, 117, [117, 2400, 1300], 150), (1, 1, 128, 300, [6000], 375), (3, 3, 128, 200, [700], 44),
+    (8, 2, 64, 513, [513, 2047], 128), (70, 10, 64, 7, [1111], 70)])
+def test_prefill_few_items(cuda_device, kind, Hq, Hkv, D, Sq, lens, pages):
+    """Short chunks after long prefixes on few heads: the key tiles of an item are cut over several CTAs, some
+    sequences of the batch having fewer tiles than there are parts."""
+    c = gen.paged_prefill_inputs(len(lens), Sq, Hq, Hkv, D, 16, lens, seed=6630 + Hq + Sq)
+    kc, vc, ks, vs = quantized(c, 16, kind)
+    bt = torch.full((len(lens), pages), -1, dtype=torch.int32)
+    bt[:, :c.block_table.shape[1]] = c.block_table
+    scale = gen.attn_scale(D)
+    o_ref, lse_ref = orc.prefill_paged_q8(c.q, kc, vc, ks, vs, bt, c.seq_lens, scale)
+    args = to(cuda_device, c.q, kc, vc, ks, vs, bt, c.seq_lens)
+    ws = torch.full((ab.binding.prefill_paged_q8_workspace_bytes(len(lens), Hkv, D, pages, 16),), 255,
+                    dtype=torch.uint8, device=cuda_device)
+    st = torch.zeros(1, dtype=torch.int32, device=cuda_device)
+    o, lse = ab.prefill_paged_q8(*args, scale=scale, workspace=ws, device_status=st)
+    assert int(st) == 0
+    compare_output(o, o_ref, lse, lse_ref, label=f"few items {kind}")
+    o2, none = ab.prefill_paged_q8(*args, scale=scale, return_lse=False)
+    assert torch.equal(o, o2) and none is None
+
+
 def test_prefill_bad_pages_and_lengths(cuda_device):
     """As the bf16 chunked prefill: keys of a page outside the pool read as zeros, a length outside
     [Sq, capacity] is clamped, both reported; the other sequences are untouched."""

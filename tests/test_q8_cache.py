@@ -224,12 +224,14 @@ def test_valid_arguments_without_a_device_report_cuda_error(lib):
 
 
 def test_prefill_workspace_bytes(lib):
-    # bf16 K and V of every page of the table, V behind K at a multiple of 256 bytes
+    # bf16 K and V of every page of the table, V behind K at a multiple of 256 bytes, and behind them an LSE and
+    # a row of fp32 O for each of 160 CTAs' 256 query rows
     up = lambda x: -(-x // 256) * 256
     for n, hkv, d, mp, ps in [(1, 1, 64, 1, 16), (4, 8, 128, 37, 16), (3, 5, 64, 3, 256)]:
         pool = n * mp * ps * hkv * d * 2
-        assert lib.attn_prefill_paged_q8_workspace_bytes(n, hkv, d, mp, ps) == up(pool) + pool
-        assert binding.prefill_paged_q8_workspace_bytes(n, hkv, d, mp, ps) == up(pool) + pool
+        want = up(up(pool) + pool) + 160 * 256 * (d + 1) * 4
+        assert lib.attn_prefill_paged_q8_workspace_bytes(n, hkv, d, mp, ps) == want
+        assert binding.prefill_paged_q8_workspace_bytes(n, hkv, d, mp, ps) == want
     for bad in [(0, 8, 128, 4, 16), (1, 0, 128, 4, 16), (1, 8, 96, 4, 16), (1, 8, 128, 0, 16), (1, 8, 128, 4, 24),
                 (2 ** 20, 8, 128, 2 ** 20, 16)]:
         assert lib.attn_prefill_paged_q8_workspace_bytes(*bad) == 0
