@@ -54,6 +54,12 @@
 // head dimension) and is rescaled there when Y grows, which is why TMEM holds only
 // the tile's own products. When the CTA's part of the sequence ends, the warpgroup
 // of its last tile adds the other's O, handed over through TMEM.
+//
+// Bound by HBM: 64 sequences of 512 to 8192 tokens (581 MB of E4M3 codes and scales, 8 KV
+// heads of 128, 4 query heads each) in 98 to 102 us with the merge, 5.7 to 5.9 TB/s; the
+// plain copy rate would take 90. One sequence of 32768 tokens (67 MB): 18.6 us, of which
+// some 8 are start-up and merge. With 8 query heads a group the softmax takes as long as
+// the copies: 32 sequences of 16384 tokens at 5.0 TB/s.
 #pragma once
 
 #include "decode.cuh"
