@@ -8,12 +8,14 @@
 // tcgen05.mma as the A operand, 128 tokens at a time, and the narrow side is
 // split into two 8-bit digits so that nothing of it is lost:
 //   S^T = Kc (128 tokens x D) * [q_hi; q_lo]^T,  q * 2^a = q_hi + q_lo / 16 (E4M3)
-//                                                        = 256 q_hi + q_lo  (int8)
+//                                          = 256 q_hi + q_lo + q_frac / 128  (int8)
 //   O^T = Vc^T (128 dims x 128 tokens) * [p_hi; p_lo]^T
 // E4M3: a bf16 value has 8 significant bits, a code 4, so two codes hold q exactly
 // down to 2^-14 of the row's largest value; the products accumulate in fp32.
-// int8: q becomes a 16-bit integer (exact down to 2^-8 of the row's largest value)
-// and every product and sum is an exact int32.
+// int8: two digits alone, a 16-bit integer, lose bits below 2^-7 of the row's largest
+// value (4e-6 of the LSE at contexts of a few tokens, 100 times an fp32 product's), so q
+// takes a third; it too is then exact down to 2^-14, and every product and sum is an
+// exact int32. With up to five query rows the third digit needs no wider product.
 // The probability that multiplies V is p_t = 2^(y_t - Y), y_t = x_t + log2(vs_t):
 // the value scale is part of the exponent, so p <= 1 whatever the scales are. Two
 // E4M3 digits keep 8 significant bits of 256 p, two int8 digits keep p to 2^-16.
@@ -105,16 +107,19 @@ struct DecodeQ8Params {
 template <int D, int NH, int GP, bool I8>
 struct DecodeQ8Smem {
   static constexpr int kR = NH * GP;                       // digit rows: head half * GP + query head
-  static constexpr int kN = kR <= 8 ? 16 : 32;             // columns of a product: hi digits, lo digits
+  static constexpr int kN = kR <= 8 ? 16 : 32;             // columns of a P V product: hi digits, lo digits
+  static constexpr int kNq = !I8 ? kN : (3 * kR + 15) / 16 * 16;   // of a score product (int8: three digits)
   static constexpr int kTileBytes = kQ8Tok * kQ8Row;       // K (or V) codes of one tile
   static constexpr int kStageBytes = 2 * kTileBytes;
   static constexpr int kQBytes = kR * D * 2;               // the query rows of an item
   static constexpr int kBlocks = kR <= 8 ? 2 : 1;          // resident CTAs per SM
-  static constexpr int kQTile = kN * kQ8Row;               // digit rows of q
+  // digit rows of q, in eights (a product of int8 with R = 8 reads the eight rows behind them as well, into
+  // columns that nothing uses)
+  static constexpr int kQTile = (!I8 || kR < 8 ? kNq : 3 * kR) * kQ8Row;
   static constexpr int kPTile = kN * kQ8Tok;               // digit rows of P
   static constexpr int kPerStage = kStageBytes + 64 * NH + 32 + 48 + 24;
   static constexpr int kFixed = 1024 + 2 * kQBytes + 2 * kQTile + 2 * kPTile + 4 * (4 * 4 * kR + 2 * 2 * 4 * kR + 2 * kR + 3 * kR) +
-                                4 * kQ8Scan + 8 * 18 + 64;
+                                8 * 18 + 64;
   static constexpr int kFit = (233472 / kBlocks - 1024 - kFixed) / kPerStage;
   static constexpr int kStages = kFit < 8 ? kFit : 8;
   static constexpr int kQT = kStages * kStageBytes;                    // q digits [item parity], 1024-byte aligned
@@ -127,21 +132,22 @@ struct DecodeQ8Smem {
   static constexpr int kMl = kYmax + 4 * 4 * 4 * kR;                   // [warpgroup][warp][kR] x {X, l} floats
   static constexpr int kQf = kMl + 4 * 2 * 2 * 4 * kR;                 // [part parity][kR] floats
   static constexpr int kSwap = kQf + 4 * 2 * kR;                       // [kR] x {X, Y, l} of the other warpgroup
-  static constexpr int kScan = (kSwap + 4 * 3 * kR + 7) / 8 * 8;         // sums of tile counts
-  static constexpr int kBars = (kScan + 4 * kQ8Scan + 7) / 8 * 8;      // mbarriers
+  static constexpr int kBars = (kSwap + 4 * 3 * kR + 7) / 8 * 8;       // mbarriers
+  static constexpr int kScan = kScales;                    // sums of tile counts, read before the first scales are copied
   // full[kStages], empty[kStages], v_go[kStages], s_full[2], s_free[2], p_ready[2], o_full[2], q_ready[2],
   // ml_ready[2], done[2], y_ready[2], swap_full, swap_free
   static constexpr int kTotal = kBars + 8 * (3 * kStages + 18);
   static constexpr int kDynamic = kTotal + 1024;
-  static constexpr int kSBuf = NH * kN;                    // columns of one score buffer: kN for each head half
+  static constexpr int kSBuf = NH * kNq;                   // columns of one score buffer: kNq for each head half
   static constexpr int kTmemSwap = 2 * kSBuf + 2 * kN;     // O of the warpgroup that does not finish a part
   static constexpr int kTmemUse = kTmemSwap + GP;
   // registers of a helper and of a softmax thread; together they are the block's launch allocation
   static constexpr int kHelperRegs = kBlocks == 1 ? 80 : 64, kSoftmaxRegs = kBlocks == 1 ? 208 : 88;
   static constexpr int kRegPool = 128 * kHelperRegs + 256 * kSoftmaxRegs;
-  static constexpr int kTmemCols = kTmemUse <= 128 ? 128 : 256;
+  static constexpr int kTmemCols = kTmemUse <= 128 ? 128 : kTmemUse <= 256 ? 256 : 512;
   static_assert(kDynamic <= 233472 / kBlocks - 1024, "shared memory per block");
   static_assert(kStages >= 3, "ring depth");
+  static_assert(kStages * (64 * NH + 32) >= 4 * kQ8Scan, "the sums lie in the scales and tile infos");
   static_assert(kQ8Scan * 4 <= kQ8Threads, "four threads a sum");
   static_assert(kTmemUse <= kTmemCols && kTmemCols * kBlocks <= 512, "tensor memory");
   static_assert(kR <= 16, "digit rows");
@@ -297,6 +303,12 @@ __device__ __forceinline__ void two_digits(float v0, float v1, uint32_t& hi, uin
     lo = e4m3x2_of((v0 - b0) * 16.f, (v1 - b1) * 16.f);
   }
 }
+// int8: what rounding two values to integers left over (half at most), in units of 1 / kQ8Frac.
+constexpr float kQ8Frac = 128.f;
+__device__ __forceinline__ uint32_t third_digits(float v0, float v1) {
+  const int i0 = __float2int_rn((v0 - rintf(v0)) * kQ8Frac), i1 = __float2int_rn((v1 - rintf(v1)) * kQ8Frac);
+  return (uint32_t(i0) & 0xFFu) | ((uint32_t(i1) & 0xFFu) << 8);
+}
 // The value of two accumulated digit columns.
 template <bool I8>
 __device__ __forceinline__ float join_digits(uint32_t hi, uint32_t lo) {
@@ -316,7 +328,7 @@ __global__ void __launch_bounds__(kQ8Threads, DecodeQ8Smem<D, NH, GP, I8>::kBloc
   using L = DecodeQ8Smem<D, NH, GP, I8>;
   launch_dependents();   // the merge is scheduled early; it waits for this grid to finish
   constexpr int NS = L::kStages;
-  constexpr int KN = L::kN;
+  constexpr int KN = L::kN, KNQ = L::kNq;
   constexpr int R = L::kR;
 
   extern __shared__ uint8_t smem_raw[];
@@ -452,6 +464,7 @@ __global__ void __launch_bounds__(kQ8Threads, DecodeQ8Smem<D, NH, GP, I8>::kBloc
       x -= __shfl_sync(0xffffffffu, incl - mine, l0);
       int t = 2 * l0;
       if (x >= scan[t]) x -= scan[t++];
+      __syncwarp();                    // the sums have been read: scales may be copied over them
       seq = t * per_entry;
       for (int units; x >= (units = q8_units(len_at(seq), p.whole)); ++seq) x -= units;
       a = x;
@@ -620,7 +633,7 @@ __global__ void __launch_bounds__(kQ8Threads, DecodeQ8Smem<D, NH, GP, I8>::kBloc
   } else if (warp == kQ8ScoreWarp) {
     // ------------------------------------------------------------ query digits and score products
     setmaxnreg_dec<L::kHelperRegs>();
-    constexpr uint32_t idesc_s = make_idesc_q8<I8>(kQ8Tok, KN, 0);   // K tile: rows = tokens, K-major
+    constexpr uint32_t idesc_s = make_idesc_q8<I8>(kQ8Tok, KNQ, 0);   // K tile: rows = tokens, K-major
     const uint64_t q_desc0 = make_sdesc_rows(smem_u32(smem + L::kQT));
     const uint64_t k_desc0 = make_sdesc_rows(smem_u32(smem));
     int slot = 0, sb = 0, qb = 1;
@@ -666,20 +679,30 @@ __global__ void __launch_bounds__(kQ8Threads, DecodeQ8Smem<D, NH, GP, I8>::kBloc
           const float up = finite ? __uint_as_float(uint32_t(sh + 127) << 23) : 0.f;
           if (part8 == 0)
             qf[r] = finite ? p.scale_log2 * __uint_as_float(uint32_t(127 - sh) << 23) : __int_as_float(0x7fc00000);
-          uint32_t hi[E / 4], lo[E / 4];
+          uint32_t hi[E / 4], lo[E / 4], frac[E / 4];
 #pragma unroll
           for (int k = 0; k < E / 4; ++k) {
-            uint32_t h0 = 0, l0 = 0, h1 = 0, l1 = 0;
+            uint32_t h0 = 0, l0 = 0, h1 = 0, l1 = 0, f0 = 0, f1 = 0;
             if (finite) {
               two_digits<I8>(bf16_lo(w[2 * k]) * up, bf16_hi(w[2 * k]) * up, h0, l0);
               two_digits<I8>(bf16_lo(w[2 * k + 1]) * up, bf16_hi(w[2 * k + 1]) * up, h1, l1);
+              if constexpr (I8) {
+                f0 = third_digits(bf16_lo(w[2 * k]) * up, bf16_hi(w[2 * k]) * up);
+                f1 = third_digits(bf16_lo(w[2 * k + 1]) * up, bf16_hi(w[2 * k + 1]) * up);
+              }
             }
             hi[k] = h0 | (h1 << 16);
             lo[k] = l0 | (l1 << 16);
+            frac[k] = f0 | (f1 << 16);
           }
           const int at = (half + nh) * 64 + part8 * E;       // byte of the row
           uint8_t* hi_at = q_tile + row_unit(r, at >> 4) + (at & 15);
           uint8_t* lo_at = q_tile + row_unit(R + r, at >> 4) + (at & 15);
+          if constexpr (I8) {
+            uint8_t* frac_at = q_tile + row_unit(2 * R + r, at >> 4) + (at & 15);
+            if constexpr (E == 16) *reinterpret_cast<uint4*>(frac_at) = make_uint4(frac[0], frac[1], frac[2], frac[3]);
+            else *reinterpret_cast<uint2*>(frac_at) = make_uint2(frac[0], frac[1]);
+          }
           if constexpr (E == 16) {
             *reinterpret_cast<uint4*>(hi_at) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
             *reinterpret_cast<uint4*>(lo_at) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
@@ -702,7 +725,7 @@ __global__ void __launch_bounds__(kQ8Threads, DecodeQ8Smem<D, NH, GP, I8>::kBloc
         for (int h = 0; h < NH; ++h)
 #pragma unroll
           for (int k = 0; k < D / 32; ++k)
-            umma_q8<I8>(tmem_s + sb * L::kSBuf + h * KN, k_desc + 2 * (h * (D / 32) + k), q_desc + 2 * (h * (D / 32) + k),
+            umma_q8<I8>(tmem_s + sb * L::kSBuf + h * KNQ, k_desc + 2 * (h * (D / 32) + k), q_desc + 2 * (h * (D / 32) + k),
                         idesc_s, k > 0);
         umma_commit(&s_full[sb]);
       }
@@ -812,20 +835,26 @@ __global__ void __launch_bounds__(kQ8Threads, DecodeQ8Smem<D, NH, GP, I8>::kBloc
       if (!wait(&s_full[wg], t_ph)) { ok = false; break; }
       tc_fence_after();
       {
-        uint32_t s_hi[R], s_lo[R];
+        uint32_t s_hi[R], s_lo[R], s_frac[R];
 #pragma unroll
         for (int n = 0; n < NH; ++n) {
-          tmem_ld_cols<GP>(my_s + n * KN + n * GP, s_hi + n * GP);
-          tmem_ld_cols<GP>(my_s + n * KN + n * GP + R, s_lo + n * GP);
+          tmem_ld_cols<GP>(my_s + n * KNQ + n * GP, s_hi + n * GP);
+          tmem_ld_cols<GP>(my_s + n * KNQ + n * GP + R, s_lo + n * GP);
+          if constexpr (I8) tmem_ld_cols<GP>(my_s + n * KNQ + n * GP + 2 * R, s_frac + n * GP);
         }
         tmem_ld_wait();
         reg_fence<R>(s_hi);
         reg_fence<R>(s_lo);
+        if constexpr (I8) reg_fence<R>(s_frac);
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(&s_free[wg]);
 #pragma unroll
-        for (int h = 0; h < R; ++h) xs[h] = valid ? join_digits<I8>(s_hi[h], s_lo[h]) * xs[h] : neg_inf;
+        for (int h = 0; h < R; ++h) {
+          float qk = join_digits<I8>(s_hi[h], s_lo[h]);
+          if constexpr (I8) qk = fmaf(float(int(s_frac[h])), 1.f / kQ8Frac, qk);
+          xs[h] = valid ? qk * xs[h] : neg_inf;
+        }
       }
       // ---- maxima: of y over the warpgroup's 128 tokens, of x over this warp's
       float* ymax = reinterpret_cast<float*>(smem + L::kYmax) + (wg * 2 + t_ph) * 4 * R;   // [row][warp]

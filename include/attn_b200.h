@@ -393,10 +393,9 @@ int attn_kv_read_q8(const void* k_codes, const void* v_codes, const float* k_sca
  *   workspace  device scratch, 16-byte aligned, contents on entry ignored, of at
  *              least attn_decode_paged_q8_workspace_bytes(Hq, Hkv, D) bytes (a
  *              few MB; 0 for arguments that the decode refuses)
- * q is split into two 8-bit digits scaled to its largest value: its elements
- * below 2^-14 (E4M3) or 2^-8 (int8) of the row's largest lose their last bits
- * (absolute error at most 2^-22 or 2^-14 of the largest). A query row with a NaN
- * or an infinity gives a NaN output row.
+ * q is split into 8-bit digits scaled to its largest value: its elements below 2^-14
+ * of the row's largest lose their last bits (absolute error at most 2^-22 of the
+ * largest). A query row with a NaN or an infinity gives a NaN output row.
  */
 size_t attn_decode_paged_q8_workspace_bytes(int Hq, int Hkv, int D);
 int attn_decode_paged_q8(const void* q, const void* k_codes, const void* v_codes, const float* k_scales,

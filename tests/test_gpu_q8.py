@@ -3,9 +3,9 @@
 
 Tolerances of decode and prefill are those of parity_util (1e-2 and one bf16 spacing on each
 output, 1e-3 on the mean and on the LSE), against the oracle on the same codes. The kernel's
-own roundings stay below them: q in two 8-bit digits is off by at most 2^-14 of the row's largest
-value (int8; 2^-22 for E4M3), so a score of D = 128 products moves by at most 2^-14 * 128 * |q| |k| scale
-< 2^-14 * 128 * 4 * 4 * 0.089 = 0.011 in the worst case of equal signs and by 1e-4 for random ones;
+own roundings stay below them: q in 8-bit digits is off by at most 2^-22 of the row's largest
+value, so a score of D = 128 products moves by at most 2^-22 * 128 * |q| |k| scale
+< 2^-22 * 128 * 4 * 4 * 0.089 = 5e-5 in the worst case of equal signs and by 5e-7 for random ones;
 P in two digits is off by at most 2^-9 of itself (E4M3) or 2^-16 (int8), which moves an output
 of a weighted mean by at most 2^-9 of max|V - O| / 2 < 1e-2 for |V| < 5."""
 
@@ -251,6 +251,26 @@ def test_decode_full_size(cuda_device, kind):
     cache = gen.paged_decode_inputs(c["N"], c["Hq"], c["Hkv"], c["D"], c["page_size"], c["len_lo"], c["len_hi"],
                                     seed=c["seed"])
     check_decode(cuda_device, cache, quantized(cache, 16, kind), f"decode full {kind}", cache.seq_lens)
+
+
+@pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("Hq,Hkv,D", [(4, 4, 128), (8, 2, 64), (16, 2, 128), (32, 2, 128), (32, 4, 64), (32, 2, 64)])
+def test_decode_lse_keeps_fp32(cuda_device, kind, Hq, Hkv, D):
+    """One token: the LSE is its score alone. q's digits are off by 2^-22 of the row's largest value (|q| < 6),
+    the products are exact in int32; E4M3 products are summed in fp32, 128 terms of at most |q k| scale < 6 * 5 *
+    0.125 that may each round by 2^-24 of the sum's size (< 16). So |error| < 128 * (6 * 2^-22 * 5 * 0.125 + 2^-24 *
+    16) = 2.4e-4 if all went one way; independent ones add up to 1 / sqrt(128) of it, 2.1e-5, and typical values
+    (|q|, |k| = 1, a few elements of q below 2^-14 of the largest, sums of size 1) to less than a tenth of that.
+    (Two int8 digits alone give an rms of 4e-6 and a maximum of 2.6e-5.)"""
+    lens = [1] * 64
+    cache = gen.paged_decode_inputs(64, Hq, Hkv, D, 16, 0, 0, seed=6470 + Hq + D, lens=lens, poison=False)
+    codes = quantized(cache, 16, kind)
+    scale = gen.attn_scale(D)
+    o_ref, lse_ref = orc.decode_paged_q8(cache.q, *codes, cache.block_table, cache.seq_lens, scale)
+    o, lse = ab.decode_paged_q8(*to(cuda_device, cache.q, *codes, cache.block_table, cache.seq_lens), scale=scale)
+    err = lse.cpu().numpy() - lse_ref
+    print(kind, "max", np.abs(err).max(), "rms", np.sqrt((err ** 2).mean()))
+    assert np.sqrt((err ** 2).mean()) < 2.1e-6 and np.abs(err).max() < 2.1e-5
 
 
 @pytest.mark.parametrize("kind", KINDS)
