@@ -583,7 +583,7 @@ def decode_paged_q8(q, k_codes, v_codes, k_scales, v_scales, block_table, seq_le
 
 
 def prefill_paged_q8_workspace_bytes(num_seqs, Hkv, D, max_pages, page_size) -> int:
-    """Workspace of prefill_paged_q8: bf16 K and V for every page of the block table."""
+    """Workspace of prefill_paged_q8: bf16 K and V for every page of the block table, and partial results."""
     return int(load_library().attn_prefill_paged_q8_workspace_bytes(num_seqs, Hkv, D, max_pages, page_size))
 
 

@@ -412,7 +412,10 @@ int attn_decode_paged_q8(const void* q, const void* k_codes, const void* v_codes
  * block and head of a group shares that one conversion. Arguments as
  * attn_prefill_paged; the workspace (16-byte aligned, contents ignored) holds at
  * least attn_prefill_paged_q8_workspace_bytes(...) bytes: bf16 K and V of
- * B * max_pages_per_seq pages, so a table trimmed to the pages in use keeps it
+ * B * max_pages_per_seq pages, and 10 (D = 64) or 21 MB for partial results: where
+ * B, Sq and Hq leave most of the GPU idle, the keys of each query block are shared
+ * out over it, by a rule on these sizes and the table's width alone (equal calls
+ * give equal bits). A table trimmed to the pages in use keeps the workspace
  * small. Returns 0 for invalid arguments or an overflowing size. A key or value
  * that reads as NaN or infinity makes o and the LSE of the queries that see it NaN
  * (all dimensions) and no others.

@@ -615,6 +615,38 @@ def test_graph_stream_and_repeats(cuda_device, kind):
     assert torch.equal(o, got[0]) and torch.equal(lse, got[1]) and not torch.equal(o, want[0])
 
 
+def test_cut_prefill_in_a_graph_and_on_two_streams(cuda_device):
+    """The prefill whose key tiles are cut (three dependent launches): captured twice into one graph with one
+    workspace, replayed on new queries, and two calls at once on two streams."""
+    c = gen.paged_prefill_inputs(2, 90, 4, 2, 128, 16, [3000, 1200], seed=6830, poison=False)
+    kc, vc, ks, vs = to(cuda_device, *quantized(c, 16, "int8"))
+    q, bt, sl = to(cuda_device, c.q, c.block_table, c.seq_lens)
+    ws = torch.empty(ab.binding.prefill_paged_q8_workspace_bytes(2, 2, 128, bt.shape[1], 16), dtype=torch.uint8,
+                     device=cuda_device)
+    q2 = q.flip(0).contiguous()
+    step = lambda: (*ab.prefill_paged_q8(q, kc, vc, ks, vs, bt, sl, workspace=ws),
+                    *ab.prefill_paged_q8(q2, kc, vc, ks, vs, bt, sl, workspace=ws))
+    want = [t.clone() for t in step()]
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        outs = step()
+    for t in (q, q2):
+        t.mul_(0.5)
+    graph.replay()
+    torch.cuda.synchronize()
+    half = [t.clone() for t in step()]
+    for a, b, w in zip(outs, half, want):
+        assert torch.equal(a, b) and not torch.equal(a, w)
+    streams = [torch.cuda.Stream(device=cuda_device) for _ in range(2)]
+    torch.cuda.synchronize()
+    rows = [[ab.prefill_paged_q8(x, kc, vc, ks, vs, bt, sl, stream=s) for x, s in zip((q, q2), streams)]
+            for _ in range(5)]
+    torch.cuda.synchronize()
+    for (o, l), (o2, l2) in rows:
+        assert torch.equal(o, half[0]) and torch.equal(l, half[1])
+        assert torch.equal(o2, half[2]) and torch.equal(l2, half[3])
+
+
 def test_two_streams_at_once(cuda_device):
     lens = [2000, 1500, 900, 40]
     cache = gen.paged_decode_inputs(4, 16, 4, 128, 16, 0, 0, seed=6810, lens=lens, poison=False)
