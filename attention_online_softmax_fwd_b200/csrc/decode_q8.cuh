@@ -945,6 +945,7 @@ __global__ void __launch_bounds__(kQ8Threads, DecodeQ8Smem<D, NH, GP, I8>::kBloc
       x_ph ^= swap ? 1u : 0u;
       uint32_t theirs[GP];
       if (!finish) {
+        tc_fence_after();   // the other warpgroup's loads of the part before are done
 #pragma unroll
         for (int h = 0; h < GP; ++h) theirs[h] = __float_as_uint(o[h]);
         tmem_st_cols<GP>(my_swap, theirs);
