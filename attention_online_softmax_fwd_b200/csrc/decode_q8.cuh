@@ -6,19 +6,26 @@
 //   O   = sum_t 2^(x_t - X) vs_t vc_t / sum_t 2^(x_t - X),   LSE = ln2 * (X + log2 sum)
 // The codes are never widened: they go from shared memory straight into
 // tcgen05.mma as the A operand, 128 tokens at a time, and the narrow side is
-// split into two 8-bit digits so that nothing of it is lost:
+// split into 8-bit digits:
 //   S^T = Kc (128 tokens x D) * [q_hi; q_lo]^T,  q * 2^a = q_hi + q_lo / 16 (E4M3)
 //                                          = 256 q_hi + q_lo + q_frac / 128  (int8)
-//   O^T = Vc^T (128 dims x 128 tokens) * [p_hi; p_lo]^T
+//   O^T = Vc^T (128 dims x 128 tokens) * [p_hi; p_lo]^T,  p likewise
 // E4M3: a bf16 value has 8 significant bits, a code 4, so two codes hold q exactly
 // down to 2^-14 of the row's largest value; the products accumulate in fp32.
 // int8: two digits alone, a 16-bit integer, lose bits below 2^-7 of the row's largest
 // value (4e-6 of the LSE at contexts of a few tokens, 100 times an fp32 product's), so q
 // takes a third; it too is then exact down to 2^-14, and every product and sum is an
 // exact int32. With up to five query rows the third digit needs no wider product.
-// The probability that multiplies V is p_t = 2^(y_t - Y), y_t = x_t + log2(vs_t):
-// the value scale is part of the exponent, so p <= 1 whatever the scales are. Two
-// E4M3 digits keep 8 significant bits of 256 p, two int8 digits keep p to 2^-16.
+// The probability that multiplies V is p_t = 2^(y_t - y), y_t = x_t + log2(vs_t) and y
+// the largest y_t of the tile: the value scale is part of the exponent, so p <= 1
+// whatever the scales are. Two E4M3 digits of 256 p are off by at most 2^-9 of p, or
+// 2^-22 where p is below 2^-13; three int8 digits of 32512 p by at most 2^-22. Both are
+// steps of a fixed size for small p, so the reference is the tile's own maximum and not
+// the running one: a heavy key takes nothing from the tokens of other tiles, and at most
+// 127 * 2^-22 of its own weight from its tile's, however long the sequence. (Against the
+// running maximum, with two digits for int8, all tokens below 2^-16 of the heaviest were
+// lost to O and kept in the sum: half of the tail of 8192 tokens behind a key of weight
+// 0.9.)
 //
 // A tile is 128 tokens x 128 bytes of K and of V: one KV head of D = 128, or two
 // neighbouring heads of D = 64 (NH = 2), whose scores come from the two halves of
@@ -53,8 +60,8 @@
 // exchange, each warp keeping a reference and accumulators of its own, O took four
 // times the registers and tensor-memory reads: 92 us instead of 73 for 16 sequences
 // of 8192 tokens with 8 query heads a group.) O stays in fp32 registers (thread =
-// head dimension) and is rescaled there when Y grows, which is why TMEM holds only
-// the tile's own products. When the CTA's part of the sequence ends, the warpgroup
+// head dimension), the tile's products are brought onto its running reference there
+// (by 2^(y - Y), Y the largest y so far), which is why TMEM holds only the tile's own. When the CTA's part of the sequence ends, the warpgroup
 // of its last tile adds the other's O, handed over through TMEM.
 //
 // Bound by HBM: 64 sequences of 512 to 8192 tokens (581 MB of E4M3 codes and scales, 8 KV
@@ -107,25 +114,26 @@ struct DecodeQ8Params {
 template <int D, int NH, int GP, bool I8>
 struct DecodeQ8Smem {
   static constexpr int kR = NH * GP;                       // digit rows: head half * GP + query head
-  static constexpr int kN = kR <= 8 ? 16 : 32;             // columns of a P V product: hi digits, lo digits
-  static constexpr int kNq = !I8 ? kN : (3 * kR + 15) / 16 * 16;   // of a score product (int8: three digits)
+  static constexpr int kN = ((I8 ? 3 : 2) * kR + 15) / 16 * 16;   // columns of a product: hi, lo (and int8's third) digits
   static constexpr int kTileBytes = kQ8Tok * kQ8Row;       // K (or V) codes of one tile
   static constexpr int kStageBytes = 2 * kTileBytes;
   static constexpr int kQBytes = kR * D * 2;               // the query rows of an item
   static constexpr int kBlocks = kR <= 8 ? 2 : 1;          // resident CTAs per SM
-  // digit rows of q, in eights (a product of int8 with R = 8 reads the eight rows behind them as well, into
-  // columns that nothing uses)
-  static constexpr int kQTile = (!I8 || kR < 8 ? kNq : 3 * kR) * kQ8Row;
-  static constexpr int kPTile = kN * kQ8Tok;               // digit rows of P
+  // query rows held: of the part at hand and the next one, or, where those would cost a stage, of one part (the
+  // next part's first tile is then copied once this part's rows are digits)
+  static constexpr int kQBufs = I8 && kR == 8 ? 1 : 2;
+  // digit rows of q and of P, in eights (a product of int8 with R = 8 reads the eight rows behind them as well,
+  // into columns that nothing uses)
+  static constexpr int kQTile = (!I8 || kR < 8 ? kN : 3 * kR) * kQ8Row, kPTile = kQTile;
   static constexpr int kPerStage = kStageBytes + 64 * NH + 32 + 48 + 24;
-  static constexpr int kFixed = 1024 + 2 * kQBytes + 2 * kQTile + 2 * kPTile + 4 * (4 * 4 * kR + 2 * 2 * 4 * kR + 2 * kR + 3 * kR) +
+  static constexpr int kFixed = 1024 + kQBufs * kQBytes + 2 * kQTile + 2 * kPTile + 4 * (4 * 4 * kR + 2 * 2 * 4 * kR + 2 * kR + 3 * kR) +
                                 8 * 18 + 64;
   static constexpr int kFit = (233472 / kBlocks - 1024 - kFixed) / kPerStage;
   static constexpr int kStages = kFit < 8 ? kFit : 8;
   static constexpr int kQT = kStages * kStageBytes;                    // q digits [item parity], 1024-byte aligned
   static constexpr int kPT = kQT + 2 * kQTile;                         // P digits [tile parity]
-  static constexpr int kQRows = kPT + 2 * kPTile;                      // query rows [part parity]
-  static constexpr int kScales = kQRows + 2 * kQBytes;                 // [stage][head half][K 8 | V 8] floats
+  static constexpr int kQRows = kPT + 2 * kPTile;                      // query rows [part parity, if two]
+  static constexpr int kScales = kQRows + kQBufs * kQBytes;                 // [stage][head half][K 8 | V 8] floats
   static constexpr int kInfo = kScales + 64 * NH * kStages;               // TileInfo per stage
   static constexpr int kJob = kInfo + 32 * kStages;                    // V copies of a stage: 8 pages, t0, byte, mask
   static constexpr int kYmax = (kJob + 48 * kStages + 15) / 16 * 16;   // [warpgroup][use parity][kR][warp] floats
@@ -138,7 +146,7 @@ struct DecodeQ8Smem {
   // ml_ready[2], done[2], y_ready[2], swap_full, swap_free
   static constexpr int kTotal = kBars + 8 * (3 * kStages + 18);
   static constexpr int kDynamic = kTotal + 1024;
-  static constexpr int kSBuf = NH * kNq;                   // columns of one score buffer: kNq for each head half
+  static constexpr int kSBuf = NH * kN;                    // columns of one score buffer: kN for each head half
   static constexpr int kTmemSwap = 2 * kSBuf + 2 * kN;     // O of the warpgroup that does not finish a part
   static constexpr int kTmemUse = kTmemSwap + GP;
   // registers of a helper and of a softmax thread; together they are the block's launch allocation
@@ -151,6 +159,7 @@ struct DecodeQ8Smem {
   static_assert(kQ8Scan * 4 <= kQ8Threads, "four threads a sum");
   static_assert(kTmemUse <= kTmemCols && kTmemCols * kBlocks <= 512, "tensor memory");
   static_assert(kR <= 16, "digit rows");
+  static_assert(kPT + 2 * kPTile + (kN * kQ8Row - kPTile) <= kTotal, "rows read behind the last digits");
 };
 
 // mbar_wait with its limit counted in clock cycles (4e9, at least two seconds): reading %globaltimer takes
@@ -288,7 +297,7 @@ __device__ __forceinline__ void e4m3x2_back(uint32_t codes, float& lo, float& hi
   lo = f16_lo(h2);
   hi = f16_hi(h2);
 }
-// Two values as two digits each: E4M3 v = hi + lo / 16, int8 (v an integer) v = 256 hi + lo.
+// Two values as two digits each: E4M3 v = hi + lo / 16, int8 v = 256 hi + lo, to the nearest integer.
 // Bytes: first value's digit in the low byte, the second's in the next.
 template <bool I8>
 __device__ __forceinline__ void two_digits(float v0, float v1, uint32_t& hi, uint32_t& lo) {
@@ -309,11 +318,13 @@ __device__ __forceinline__ uint32_t third_digits(float v0, float v1) {
   const int i0 = __float2int_rn((v0 - rintf(v0)) * kQ8Frac), i1 = __float2int_rn((v1 - rintf(v1)) * kQ8Frac);
   return (uint32_t(i0) & 0xFFu) | ((uint32_t(i1) & 0xFFu) << 8);
 }
-// The value of two accumulated digit columns.
+// The value of the accumulated digit columns (E4M3 has no third one).
 template <bool I8>
-__device__ __forceinline__ float join_digits(uint32_t hi, uint32_t lo) {
-  if constexpr (I8) return float(int(hi) * 256 + int(lo));   // |.| < 2^30: 128 products of at most 2^15 * 2^7
-  else return fmaf(__uint_as_float(lo), 0.0625f, __uint_as_float(hi));
+__device__ __forceinline__ float join_digits(uint32_t hi, uint32_t lo, uint32_t frac) {
+  if constexpr (I8)   // |256 hi + lo| < 2^30: 128 products of at most 2^15 * 2^7
+    return fmaf(float(int(frac)), 1.f / kQ8Frac, float(int(hi) * 256 + int(lo)));
+  else
+    return fmaf(__uint_as_float(lo), 0.0625f, __uint_as_float(hi));
 }
 
 // Units of work of a sequence of (clamped) length `len`: its tiles, or one for all of it.
@@ -328,7 +339,7 @@ __global__ void __launch_bounds__(kQ8Threads, DecodeQ8Smem<D, NH, GP, I8>::kBloc
   using L = DecodeQ8Smem<D, NH, GP, I8>;
   launch_dependents();   // the merge is scheduled early; it waits for this grid to finish
   constexpr int NS = L::kStages;
-  constexpr int KN = L::kN, KNQ = L::kNq;
+  constexpr int KN = L::kN;
   constexpr int R = L::kR;
 
   extern __shared__ uint8_t smem_raw[];
@@ -546,9 +557,10 @@ __global__ void __launch_bounds__(kQ8Threads, DecodeQ8Smem<D, NH, GP, I8>::kBloc
       const bool first = t0 == w.t_begin;
       int* job = reinterpret_cast<int*>(smem + L::kJob) + slot * 12;
       ok = __all_sync(0xffffffffu, q8_wait(&empty[slot], phase ^ 1u, abort_flag, p.status));
-      // the query rows of the part before the previous one have been turned into digits
-      if (first && part_no >= 2)
-        ok = __all_sync(0xffffffffu, ok && q8_wait(&q_ready[part_no & 1], uint32_t((part_no - 2) >> 1) & 1u, abort_flag, p.status));
+      // the query rows that the part's own are copied over have been turned into digits
+      const int q_before = part_no - L::kQBufs;
+      if (first && q_before >= 0)
+        ok = __all_sync(0xffffffffu, ok && q8_wait(&q_ready[q_before & 1], uint32_t(q_before >> 1) & 1u, abort_flag, p.status));
       if (!ok) break;
       if (lane < 8) job[lane] = page;
       if (lane == 0) {
@@ -567,7 +579,7 @@ __global__ void __launch_bounds__(kQ8Threads, DecodeQ8Smem<D, NH, GP, I8>::kBloc
         const uint32_t qbytes = first ? uint32_t(q_rows * D * 2) : 0u;
         mbar_arrive_expect_tx(&full[slot], uint32_t(__popc(box_mask)) * uint32_t(2 * kQ8Row * p.box) + qbytes);
         if (first)
-          bulk_load(smem + L::kQRows + (part_no & 1) * L::kQBytes, p.q + (size_t(w.seq) * p.Hq + size_t(head0) * p.G) * D, qbytes,
+          bulk_load(smem + L::kQRows + (part_no & (L::kQBufs - 1)) * L::kQBytes, p.q + (size_t(w.seq) * p.Hq + size_t(head0) * p.G) * D, qbytes,
                     &full[slot]);
       }
       __syncwarp();
@@ -633,7 +645,7 @@ __global__ void __launch_bounds__(kQ8Threads, DecodeQ8Smem<D, NH, GP, I8>::kBloc
   } else if (warp == kQ8ScoreWarp) {
     // ------------------------------------------------------------ query digits and score products
     setmaxnreg_dec<L::kHelperRegs>();
-    constexpr uint32_t idesc_s = make_idesc_q8<I8>(kQ8Tok, KNQ, 0);   // K tile: rows = tokens, K-major
+    constexpr uint32_t idesc_s = make_idesc_q8<I8>(kQ8Tok, KN, 0);   // K tile: rows = tokens, K-major
     const uint64_t q_desc0 = make_sdesc_rows(smem_u32(smem + L::kQT));
     const uint64_t k_desc0 = make_sdesc_rows(smem_u32(smem));
     int slot = 0, sb = 0, qb = 1;
@@ -658,7 +670,7 @@ __global__ void __launch_bounds__(kQ8Threads, DecodeQ8Smem<D, NH, GP, I8>::kBloc
           const int i = min(i0 + (lane >> 3), n_rows - 1);   // a repeated last row writes the same again
           const int nh = NH == 2 && i >= p.G ? 1 : 0;
           const int r = nh * GP + (i - nh * p.G);            // digit row
-          const uint4* src = reinterpret_cast<const uint4*>(smem + L::kQRows + qb * L::kQBytes + (i * D + part8 * E) * 2);
+          const uint4* src = reinterpret_cast<const uint4*>(smem + L::kQRows + (qb & (L::kQBufs - 1)) * L::kQBytes + (i * D + part8 * E) * 2);
           uint32_t w[E / 2];
           uint32_t top = 0;
 #pragma unroll
@@ -725,7 +737,7 @@ __global__ void __launch_bounds__(kQ8Threads, DecodeQ8Smem<D, NH, GP, I8>::kBloc
         for (int h = 0; h < NH; ++h)
 #pragma unroll
           for (int k = 0; k < D / 32; ++k)
-            umma_q8<I8>(tmem_s + sb * L::kSBuf + h * KNQ, k_desc + 2 * (h * (D / 32) + k), q_desc + 2 * (h * (D / 32) + k),
+            umma_q8<I8>(tmem_s + sb * L::kSBuf + h * KN, k_desc + 2 * (h * (D / 32) + k), q_desc + 2 * (h * (D / 32) + k),
                         idesc_s, k > 0);
         umma_commit(&s_full[sb]);
       }
@@ -787,12 +799,12 @@ __global__ void __launch_bounds__(kQ8Threads, DecodeQ8Smem<D, NH, GP, I8>::kBloc
     uint32_t phase = 0, t_ph = 0, m_ph = 0, x_ph = 0;
     bool ok = true;
     int part_no = -1;
-    float X[R], Y[R], l[R];   // X of this warp's tokens, Y of the warpgroup's, l of this thread's
-    float o[GP];
+    float X[R], l[R];         // X of this warp's tokens, l of this thread's
+    float Y[GP], o[GP];       // O of this thread's dimension against the warpgroup's Y
 #pragma unroll
-    for (int h = 0; h < R; ++h) { X[h] = Y[h] = kFloor; l[h] = 0.f; }
+    for (int h = 0; h < R; ++h) { X[h] = kFloor; l[h] = 0.f; }
 #pragma unroll
-    for (int h = 0; h < GP; ++h) o[h] = 0.f;
+    for (int h = 0; h < GP; ++h) { Y[h] = kFloor; o[h] = 0.f; }
     auto wait = [&](uint64_t* bar, uint32_t ph) -> bool {   // the same answer in the whole warp
       return __all_sync(0xffffffffu, q8_wait(bar, ph, abort_flag, p.status));
     };
@@ -807,9 +819,9 @@ __global__ void __launch_bounds__(kQ8Threads, DecodeQ8Smem<D, NH, GP, I8>::kBloc
         part_no = ti.len;
         if (!wait(&q_ready[q_par], uint32_t(part_no >> 1) & 1u)) { ok = false; break; }
 #pragma unroll
-        for (int h = 0; h < R; ++h) { X[h] = Y[h] = kFloor; l[h] = 0.f; }
+        for (int h = 0; h < R; ++h) { X[h] = kFloor; l[h] = 0.f; }
 #pragma unroll
-        for (int h = 0; h < GP; ++h) o[h] = 0.f;
+        for (int h = 0; h < GP; ++h) { Y[h] = kFloor; o[h] = 0.f; }
       }
       const bool valid = tok < ti.ntok && !((ti.bad >> (tok >> 4)) & 1);
       if (!valid) {   // a V row that was not copied: 0 * (stale bytes) must not reach O
@@ -838,9 +850,9 @@ __global__ void __launch_bounds__(kQ8Threads, DecodeQ8Smem<D, NH, GP, I8>::kBloc
         uint32_t s_hi[R], s_lo[R], s_frac[R];
 #pragma unroll
         for (int n = 0; n < NH; ++n) {
-          tmem_ld_cols<GP>(my_s + n * KNQ + n * GP, s_hi + n * GP);
-          tmem_ld_cols<GP>(my_s + n * KNQ + n * GP + R, s_lo + n * GP);
-          if constexpr (I8) tmem_ld_cols<GP>(my_s + n * KNQ + n * GP + 2 * R, s_frac + n * GP);
+          tmem_ld_cols<GP>(my_s + n * KN + n * GP, s_hi + n * GP);
+          tmem_ld_cols<GP>(my_s + n * KN + n * GP + R, s_lo + n * GP);
+          if constexpr (I8) tmem_ld_cols<GP>(my_s + n * KN + n * GP + 2 * R, s_frac + n * GP);
         }
         tmem_ld_wait();
         reg_fence<R>(s_hi);
@@ -851,9 +863,7 @@ __global__ void __launch_bounds__(kQ8Threads, DecodeQ8Smem<D, NH, GP, I8>::kBloc
         if (lane == 0) mbar_arrive(&s_free[wg]);
 #pragma unroll
         for (int h = 0; h < R; ++h) {
-          float qk = join_digits<I8>(s_hi[h], s_lo[h]);
-          if constexpr (I8) qk = fmaf(float(int(s_frac[h])), 1.f / kQ8Frac, qk);
-          xs[h] = valid ? qk * xs[h] : neg_inf;
+          xs[h] = valid ? join_digits<I8>(s_hi[h], s_lo[h], s_frac[h]) * xs[h] : neg_inf;
         }
       }
       // ---- maxima: of y over the warpgroup's 128 tokens, of x over this warp's
@@ -875,17 +885,13 @@ __global__ void __launch_bounds__(kQ8Threads, DecodeQ8Smem<D, NH, GP, I8>::kBloc
         l[h] += fast_exp2(xs[h] - X[h]);
       }
       if (!wait(&y_ready[wg], t_ph)) { ok = false; break; }
+      float y[R];   // the tile's reference
 #pragma unroll
       for (int h = 0; h < R; ++h) {
         const float4 t = *reinterpret_cast<const float4*>(ymax + 4 * h);
-        const float ty = max_nan(Y[h], max_nan(max_nan(t.x, t.y), max_nan(t.z, t.w)));
-        if (!(ty == Y[h])) {   // the same in the whole warpgroup
-          const float a = fast_exp2(Y[h] - ty);
-          Y[h] = ty;
-          if (NH == 1 || h / GP == my_half) o[h % GP] *= a;
-        }
+        y[h] = max_nan(kFloor, max_nan(max_nan(t.x, t.y), max_nan(t.z, t.w)));
       }
-      // ---- P digits: row h (hi) and R + h (lo), this token's byte
+      // ---- P digits: rows h (hi), R + h (lo) and, int8, 2 R + h (third), this token's byte
       {
         const int unit = 2 * ww + (lane >> 4), b = lane & 15;
 #pragma unroll
@@ -893,14 +899,15 @@ __global__ void __launch_bounds__(kQ8Threads, DecodeQ8Smem<D, NH, GP, I8>::kBloc
           float pv[2] = {0.f, 0.f};
 #pragma unroll
           for (int k = 0; k < 2 && h + k < R; ++k)
-            pv[k] = fast_exp2(xs[h + k] + lvs[(h + k) / GP] - Y[h + k]) * kPScale;
-          uint32_t hi, lo;
+            pv[k] = fast_exp2(xs[h + k] + lvs[(h + k) / GP] - y[h + k]) * kPScale;
+          uint32_t hi, lo, frac = 0;
           two_digits<I8>(pv[0], pv[1], hi, lo);
-          p_tile[row_unit(h, unit) + b] = uint8_t(hi);
-          p_tile[row_unit(R + h, unit) + b] = uint8_t(lo);
-          if (h + 1 < R) {
-            p_tile[row_unit(h + 1, unit) + b] = uint8_t(hi >> 8);
-            p_tile[row_unit(R + h + 1, unit) + b] = uint8_t(lo >> 8);
+          if constexpr (I8) frac = third_digits(pv[0], pv[1]);
+#pragma unroll
+          for (int k = 0; k < 2 && h + k < R; ++k) {
+            p_tile[row_unit(h + k, unit) + b] = uint8_t(hi >> (8 * k));
+            p_tile[row_unit(R + h + k, unit) + b] = uint8_t(lo >> (8 * k));
+            if constexpr (I8) p_tile[row_unit(2 * R + h + k, unit) + b] = uint8_t(frac >> (8 * k));
           }
         }
       }
@@ -913,14 +920,22 @@ __global__ void __launch_bounds__(kQ8Threads, DecodeQ8Smem<D, NH, GP, I8>::kBloc
       if (!wait(&o_full[wg], t_ph)) { ok = false; break; }
       tc_fence_after();
       {
-        uint32_t hi[GP], lo[GP];
+        uint32_t hi[GP], lo[GP], frac[GP];
         tmem_ld_cols<GP>(my_o, hi);
         tmem_ld_cols<GP>(my_o + R, lo);
+        if constexpr (I8) tmem_ld_cols<GP>(my_o + 2 * R, frac);
         tmem_ld_wait();
         reg_fence<GP>(hi);
         reg_fence<GP>(lo);
+        if constexpr (I8) reg_fence<GP>(frac);
 #pragma unroll
-        for (int h = 0; h < GP; ++h) o[h] += join_digits<I8>(hi[h], lo[h]);
+        for (int h = 0; h < GP; ++h) {
+          const float v = join_digits<I8>(hi[h], lo[h], frac[h]);
+          const float yt = NH == 2 && my_half ? y[(NH - 1) * GP + h] : y[h];
+          const float d = yt - Y[h], a = fast_exp2(-fabsf(d));   // the lower reference's onto the higher one
+          o[h] = d > 0.f ? fmaf(o[h], a, v) : fmaf(v, a, o[h]);
+          Y[h] = max_nan(Y[h], yt);
+        }
         tc_fence_before();
       }
       slot += 2;
@@ -964,8 +979,8 @@ __global__ void __launch_bounds__(kQ8Threads, DecodeQ8Smem<D, NH, GP, I8>::kBloc
       const bool writer = (ww & (NH == 2 ? 1 : 3)) == 0 && lane == 0;   // one thread of each head half
 #pragma unroll
       for (int h = 0; h < GP; ++h) {
-        const int r = NH == 2 && my_half ? GP + h : h;   // the row's number, and its Y: not an index of registers
-        const float yh = NH == 2 && my_half ? Y[(NH - 1) * GP + h] : Y[h];
+        const int r = NH == 2 && my_half ? GP + h : h;   // the row's number
+        const float yh = Y[h];
         float mx = kFloor, lsum = 0.f;
 #pragma unroll
         for (int w = 0; w < 4; ++w) mx = max_nan(mx, ml[(w * R + r) * 2]);
