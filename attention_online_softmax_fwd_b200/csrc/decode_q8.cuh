@@ -1000,8 +1000,10 @@ __global__ void __launch_bounds__(kQ8Threads, DecodeQ8Smem<D, NH, GP, I8>::kBloc
         const float my = max_nan(yh, oy);
         float v = o[h] * fast_exp2(yh - my);
         if (swap) v = fmaf(__uint_as_float(theirs[h]), fast_exp2(oy - my), v);
-        // lsum is 0 only if every page was invalid; a NaN stays a NaN
-        v = lsum == 0.f ? 0.f : __fdividef(v * fast_exp2(my - mx) * (1.f / kPScale), lsum);
+        // lsum is 0 only if every page was invalid; a NaN stays a NaN. The digits' factor and the sum go first and
+        // the V scale's exponent in two halves, so that nothing on the way is beyond the result's own range
+        const float up = fast_exp2(0.5f * (my - mx));
+        v = lsum == 0.f ? 0.f : __fdividef(v * (1.f / kPScale), lsum) * up * up;
         const float lse2 = lsum == 0.f ? neg_inf : mx + __log2f(lsum);
         if (h >= p.G || !mine) continue;
         if (part < 0) {
@@ -1057,6 +1059,9 @@ __global__ void __launch_bounds__(128) decode_q8_merge_kernel(const DecodeQ8Para
   auto part_row = [&](int i) {
     return size_t(((first + i) * p.team + team_lane) * 2 + (i == 0 ? cut.w : 0)) * p.part_rows + r;
   };
+  // weights are at most 1 / kQ8MaxCtas: a sum of parts is no larger than the largest of them
+  constexpr float kLog2Parts = 9.f, kWeight = 1.f / 512.f;
+  static_assert(kQ8MaxCtas <= 512, "parts of a sequence");
   float m = neg_inf, sum = 0.f, acc[E];
 #pragma unroll
   for (int e = 0; e < E; ++e) acc[e] = 0.f;
@@ -1064,7 +1069,7 @@ __global__ void __launch_bounds__(128) decode_q8_merge_kernel(const DecodeQ8Para
     const int k1 = min(16, n - i0);
     const float lse = lane < k1 ? p.ws_lse[part_row(i0 + lane)] : neg_inf;
     const float mx = max_nan(m, warp_max_nan(lse)), off = mx == neg_inf ? 0.f : mx;
-    const float old = fast_exp2(m - off), w = fast_exp2(lse - off);
+    const float old = fast_exp2(m - off), w = fast_exp2(lse - off) * kWeight;
     m = mx;
     sum = fmaf(sum, old, w);                     // this lane's part of the sum
 #pragma unroll
@@ -1119,7 +1124,7 @@ __global__ void __launch_bounds__(128) decode_q8_merge_kernel(const DecodeQ8Para
   for (int e = 0; e < E / 2; ++e) out[e] = pack_bf16x2(acc[2 * e] * inv, acc[2 * e + 1] * inv);
   if constexpr (E == 4) *reinterpret_cast<uint2*>(p.o + at * D + lane * E) = make_uint2(out[0], out[1]);
   else *reinterpret_cast<uint32_t*>(p.o + at * D + lane * E) = out[0];
-  if (p.lse && lane == 0) p.lse[at] = sum == 0.f ? neg_inf : (m + __log2f(sum)) * 0.69314718055994531f;
+  if (p.lse && lane == 0) p.lse[at] = sum == 0.f ? neg_inf : (m + (__log2f(sum) + kLog2Parts)) * 0.69314718055994531f;
 }
 
 }  // namespace attn
