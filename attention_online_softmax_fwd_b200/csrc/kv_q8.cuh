@@ -264,7 +264,8 @@ __device__ __forceinline__ bool q8_not_finite(const uint4& w) {
 // For the prefill (pad > 0) a value that is not finite becomes zero and its key NaN:
 // a hidden key's score is replaced, whatever it is, but a hidden value is multiplied
 // by a zero in the tensor cores, and would reach the chunk's earlier queries. The
-// queries that see the token are NaN either way.
+// queries that see the token are NaN either way. A key that is infinite (scale times
+// code past the largest number) becomes NaN as well: a score of -inf would only hide it.
 template <int D, bool I8>
 __global__ void __launch_bounds__(256) kv_read_q8_kernel(const KvReadQ8Params p) {
   const int b = int(blockIdx.x / unsigned(p.ctas_per_seq)), part = int(blockIdx.x % unsigned(p.ctas_per_seq));
@@ -311,9 +312,10 @@ __global__ void __launch_bounds__(256) kv_read_q8_kernel(const KvReadQ8Params p)
         const int i = i0 + u * group;
         if (i >= vecs) continue;
         uint4 kw = q8_widen8<I8>(k[u], ks[u]), vw = q8_widen8<I8>(v[u], vs[u]);
-        if (p.pad && q8_not_finite(vw)) {
-          kw = make_uint4(0x7FC07FC0u, 0x7FC07FC0u, 0x7FC07FC0u, 0x7FC07FC0u);
-          vw = make_uint4(0, 0, 0, 0);
+        if (p.pad) {
+          const bool bad_v = q8_not_finite(vw);
+          if (bad_v || q8_not_finite(kw)) kw = make_uint4(0x7FC07FC0u, 0x7FC07FC0u, 0x7FC07FC0u, 0x7FC07FC0u);
+          if (bad_v) vw = make_uint4(0, 0, 0, 0);
         }
         ko[i] = kw;
         vo[i] = vw;
