@@ -62,6 +62,23 @@ __device__ __forceinline__ uint32_t q8_codes2(float a, float b) {
     return r;
   }
 }
+// x / s and a * b rounded to odd (truncated, the last bit set where something was cut off): rounding that
+// again, to a code's few bits, is as good as rounding the exact number. For scales that are no powers of two.
+__device__ __forceinline__ float q8_odd(float truncated, float rest) {
+  return rest != 0.f ? __uint_as_float(__float_as_uint(truncated) | 1u) : truncated;
+}
+__device__ __forceinline__ float q8_div_odd(float x, float s) {
+  const float q = __fdiv_rz(x, s);
+  return q8_odd(q, fmaf(-q, s, x));
+}
+__device__ __forceinline__ float q8_mul_odd(float a, float b) {
+  const float m = __fmul_rz(a, b);
+  return q8_odd(m, fmaf(a, b, -m));
+}
+// int8: a value beyond the codes that are written (-127 .. 127) becomes the last of them.
+template <bool I8>
+__device__ __forceinline__ float q8_clamp(float v) { return I8 ? fminf(fmaxf(v, -127.f), 127.f) : v; }
+
 // Four codes -> four values (not yet multiplied by the scale).
 template <bool I8>
 __device__ __forceinline__ void q8_values4(uint32_t four, float (&v)[4]) {
@@ -188,35 +205,56 @@ __global__ void __launch_bounds__(256, SEGS == 1 ? 4 : 2) kv_append_q8_kernel(co
           float a[4], c[4];
           q8_values4<I8>(old.x, a);
           q8_values4<I8>(old.y, c);
-          uint2 out;
-          out.x = q8_codes2<I8>(a[0] * ratio, a[1] * ratio) | (q8_codes2<I8>(a[2] * ratio, a[3] * ratio) << 16);
-          out.y = q8_codes2<I8>(c[0] * ratio, c[1] * ratio) | (q8_codes2<I8>(c[2] * ratio, c[3] * ratio) << 16);
-          *at = out;
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {   // another writer's codes may hold -128, and its scale any bits
+            a[e] = q8_clamp<I8>(q8_mul_odd(a[e], ratio));
+            c[e] = q8_clamp<I8>(q8_mul_odd(c[e], ratio));
+          }
+          *at = make_uint2(q8_codes2<I8>(a[0], a[1]) | (q8_codes2<I8>(a[2], a[3]) << 16),
+                           q8_codes2<I8>(c[0], c[1]) | (q8_codes2<I8>(c[2], c[3]) << 16));
         }
     }
-    if (I8 && amax > 0x7F7E0000u) {   // above 127 * 2^121: the scale could not grow, the values saturate there
+    // ---- the new tokens' codes
+    if (scale == scale && (__float_as_uint(scale) & 0x7FFFFFu) != 0) {
+      // a block begun by another writer, whose scale is no power of two: x * inv would round twice. Rare, so the
+      // tokens are read again, and the common path keeps its registers
+#pragma unroll 1
+      for (int n = 0; n < SEGS * PASSES; ++n) {
+        const int slot = (n / PASSES * wpu + wi) * 16 + n % PASSES * RPP + row_in_pass;
+        if (slot < begin || slot >= stop) continue;
+        const uint4 t = __ldg(reinterpret_cast<const uint4*>(new_rows + (long long)slot * row_elems));
+        const uint32_t w[4] = {t.x, t.y, t.z, t.w};
+        uint32_t q[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          q[e] = q8_codes2<I8>(q8_clamp<I8>(q8_div_odd(bf16_lo(w[e]), scale)), q8_clamp<I8>(q8_div_odd(bf16_hi(w[e]), scale)));
+        *reinterpret_cast<uint2*>(codes + size_t(slot) * p.Hkv * D + col) =
+            make_uint2(q[0] | (q[1] << 16), q[2] | (q[3] << 16));
+      }
+    } else {
+      if (I8 && amax > 0x7F7E0000u) {   // above 127 * 2^121: the scale could not grow, the values saturate there
+#pragma unroll
+        for (int g = 0; g < SEGS; ++g)
+#pragma unroll
+          for (int i = 0; i < PASSES; ++i) {
+            x[g][i].x = q8_saturate(x[g][i].x); x[g][i].y = q8_saturate(x[g][i].y);
+            x[g][i].z = q8_saturate(x[g][i].z); x[g][i].w = q8_saturate(x[g][i].w);
+          }
+      }
 #pragma unroll
       for (int g = 0; g < SEGS; ++g)
 #pragma unroll
         for (int i = 0; i < PASSES; ++i) {
-          x[g][i].x = q8_saturate(x[g][i].x); x[g][i].y = q8_saturate(x[g][i].y);
-          x[g][i].z = q8_saturate(x[g][i].z); x[g][i].w = q8_saturate(x[g][i].w);
+          const int slot = (g * wpu + wi) * 16 + i * RPP + row_in_pass;
+          if (slot < begin || slot >= stop) continue;
+          const uint32_t w[4] = {x[g][i].x, x[g][i].y, x[g][i].z, x[g][i].w};
+          uint32_t q[4];
+#pragma unroll
+          for (int e = 0; e < 4; ++e) q[e] = q8_codes2<I8>(bf16_lo(w[e]) * inv, bf16_hi(w[e]) * inv);
+          *reinterpret_cast<uint2*>(codes + size_t(slot) * p.Hkv * D + col) =
+              make_uint2(q[0] | (q[1] << 16), q[2] | (q[3] << 16));
         }
     }
-    // ---- the new tokens' codes
-#pragma unroll
-    for (int g = 0; g < SEGS; ++g)
-#pragma unroll
-      for (int i = 0; i < PASSES; ++i) {
-        const int slot = (g * wpu + wi) * 16 + i * RPP + row_in_pass;
-        if (slot < begin || slot >= stop) continue;
-        const uint32_t w[4] = {x[g][i].x, x[g][i].y, x[g][i].z, x[g][i].w};
-        uint32_t q[4];
-#pragma unroll
-        for (int e = 0; e < 4; ++e) q[e] = q8_codes2<I8>(bf16_lo(w[e]) * inv, bf16_hi(w[e]) * inv);
-        *reinterpret_cast<uint2*>(codes + size_t(slot) * p.Hkv * D + col) =
-            make_uint2(q[0] | (q[1] << 16), q[2] | (q[3] << 16));
-      }
     if (lane == 0 && wi == 0) *scale_at = scale;
   }
 }

@@ -76,3 +76,43 @@ def test_prefill_key_that_reads_as_infinity(cuda_device, D, Hq, Hkv, Sq, pages):
     assert np.isnan(o[bad]).all() and np.isnan(lse.transpose(0, 2, 1)[bad]).all()
     compare_output(o, np.where(bad[..., None], 0.0, o_ref), mask=np.repeat(~bad[..., None], D, -1))
     assert np.abs(lse - l_ref)[~bad.transpose(0, 2, 1)].max() <= 1e-3
+
+
+@pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("D,Hkv,page,block", [(128, 2, 16, 16), (64, 3, 64, 32), (128, 1, 256, 256)])
+def test_append_to_blocks_with_foreign_scales(cuda_device, kind, D, Hkv, page, block):
+    """Blocks begun by another writer, with scales that are no powers of two: new codes are x / s rounded once,
+    ties to even, and earlier codes c s / s' rounded once. Equal to the oracle code for code."""
+    g = torch.Generator().manual_seed(7500 + D + block)
+    N, T = 6, 7
+    P = N + 1
+    qmax = 448.0 if kind == "e4m3" else 127.0
+    if kind == "e4m3":
+        kc = torch.randint(0, 256, (P, page, Hkv, D), generator=g, dtype=torch.int32)
+        kc = torch.where((kc & 127) == 127, kc - 1, kc).to(torch.uint8)
+    else:
+        kc = torch.randint(-128, 128, (P, page, Hkv, D), generator=g, dtype=torch.int32).to(torch.int8)
+    vc = kc.flip(0).contiguous()
+    odd = torch.tensor([3.0, 5.0, 7.0, 11.0, 1.0 / 3.0, 0.3])
+    ks = odd[torch.randint(0, 6, (P, page // block, Hkv), generator=g)] * 2.0 ** -8
+    vs = torch.rand(P, page // block, Hkv, generator=g) * 0.01 + 1e-4
+    ks[5], vs[5] = 2e38, 3.3e38                          # the reciprocals are not normal numbers
+    bt = torch.randperm(N, generator=g).to(torch.int32)[:, None]
+    starts = np.array([3, 1, 9, 5, 2, 8])
+    # K: halves of small multiples of the scales (ties), below the block's scale; V: some blocks grow, some stay
+    page_of = bt[:, 0].long()
+    n = torch.randint(0, 21, (N, T, Hkv, D), generator=g) * 2 + 1
+    base = torch.tensor([3.0, 5.0, 7.0, 11.0])[torch.randint(0, 4, (N, T, Hkv, D), generator=g)]
+    kn = (n * base * 2.0 ** -9 * torch.where(torch.rand(n.shape, generator=g) < 0.5, 1, -1)).to(torch.bfloat16)
+    vn = (torch.randn(N, T, Hkv, D, generator=g) * torch.exp2(torch.randint(-6, 6, (N, 1, Hkv, 1), generator=g).float())
+          ).to(torch.bfloat16)
+    kn[page_of == 5] = 1e38
+    vn[page_of == 5] = -2e38
+    want = orc.kv_append_q8(kc, vc, ks, vs, bt, starts, kn, vn)
+    kcd, vcd, ksd, vsd, knd, vnd, btd = to(cuda_device, kc, vc, ks, vs, kn, vn, bt)
+    ab.kv_append_q8(knd, vnd, kcd, vcd, ksd, vsd, btd, torch.tensor(starts, dtype=torch.int32, device=cuda_device))
+    before = ks[page_of, 0].double().numpy()
+    assert (want[2][page_of.numpy(), 0] == before).any()                         # some foreign scales are kept
+    for got, ref in zip((ksd, vsd, kcd, vcd), (want[2], want[3], want[0], want[1])):
+        diff = got.cpu().numpy() != ref.astype(got.cpu().numpy().dtype)
+        assert not diff.any(), f"{int(diff.sum())} of {diff.size} differ"
