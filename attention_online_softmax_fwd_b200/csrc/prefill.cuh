@@ -1161,7 +1161,7 @@ __global__ void __launch_bounds__(128) prefill_merge_kernel(const PrefillParams 
 #pragma unroll
     for (int e = 0; e < E; ++e) acc[e] = fmaf(wt, v[e], acc[e]);
   }
-  const float inv = 1.f / sum;                              // every row sees a key: its own
+  const float inv = sum == 0.f ? 0.f : 1.f / sum;           // 0: every score it sees is -inf, as in the uncut kernel
   uint32_t out[E / 2];
 #pragma unroll
   for (int e = 0; e < E / 2; ++e) out[e] = pack_bf16x2(acc[2 * e] * inv, acc[2 * e + 1] * inv);

@@ -116,3 +116,20 @@ def test_append_to_blocks_with_foreign_scales(cuda_device, kind, D, Hkv, page, b
     for got, ref in zip((ksd, vsd, kcd, vcd), (want[2], want[3], want[0], want[1])):
         diff = got.cpu().numpy() != ref.astype(got.cpu().numpy().dtype)
         assert not diff.any(), f"{int(diff.sum())} of {diff.size} differ"
+
+
+@pytest.mark.parametrize("D", [64, 128])
+def test_prefill_row_without_a_finite_score(cuda_device, D):
+    """A query whose only scores pass the largest number downwards: o = 0 and an LSE of -inf, whether or not the
+    table is wide enough for the keys to be cut over several CTAs."""
+    kc = torch.full((2, 16, 1, D), 0x7E, dtype=torch.uint8)          # 448 * 2^119, a finite bf16
+    vc = torch.full((2, 16, 1, D), 0x38, dtype=torch.uint8)          # 1
+    ks, vs = torch.full((2, 1, 1), 2.0 ** 119), torch.ones(2, 1, 1)
+    q = torch.full((2, 1, 2, D), -100.0, dtype=torch.bfloat16)
+    q[1] = 2.0 ** -120                                               # the second sequence's scores are ordinary ones
+    for pages in (1, 200):
+        bt = torch.full((2, pages), -1, dtype=torch.int32)
+        bt[:, 0] = torch.tensor([0, 1])
+        o, lse = ab.prefill_paged_q8(*to(cuda_device, q, kc, vc, ks, vs, bt, torch.tensor([1, 5], dtype=torch.int32)))
+        assert (o[0] == 0).all() and torch.isneginf(lse[0]).all()
+        assert (o[1] == 1).all() and torch.isfinite(lse[1]).all()
