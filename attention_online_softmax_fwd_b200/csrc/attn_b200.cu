@@ -735,7 +735,8 @@ bool prefill_q8_layout(int num_seqs, int Hkv, int D, int page_size, int max_page
 
 // Parts that each item's key tiles are cut into, so that few items fill the SMs. A tile costs a CTA about
 // 1.3 us, the parts and their merge some 3 us and 2.5 us of the host's time, so items are cut if that saves
-// the longest of them more than four tiles (a table of key_tiles tiles, all of them in use). 32 query heads of
+// the longest of them more than four tiles (a table of key_tiles tiles, all of them in use: the lengths are on
+// the device, so short sequences behind a wide table are cut as well, into single tiles). 32 query heads of
 // 128, one sequence of 100 new tokens: 2048 tokens 33.2 us whole and 21.8 cut, 8192 tokens 103 and 43.5; four
 // heads, 16384 tokens: 186 and 26.8. Two sequences of 1000 tokens (64 items, 8 tiles in two parts) 23.2 and 25.2.
 int prefill_q8_splits(int items, int sms, long long key_tiles) {

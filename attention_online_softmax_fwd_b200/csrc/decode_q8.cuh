@@ -58,17 +58,20 @@
 // at a time. The four warps of a warpgroup exchange the tile's maxima of y once, so
 // that its 128 tokens share one reference and P V is one accumulation. (Without the
 // exchange, each warp keeping a reference and accumulators of its own, O took four
-// times the registers and tensor-memory reads: 92 us instead of 73 for 16 sequences
-// of 8192 tokens with 8 query heads a group.) O stays in fp32 registers (thread =
+// times the registers and tensor-memory reads: 92 us instead of 73, when it was tried, for
+// 16 sequences of 8192 tokens with 8 query heads a group.) O stays in fp32 registers (thread =
 // head dimension), the tile's products are brought onto its running reference there
 // (by 2^(y - Y), Y the largest y so far), which is why TMEM holds only the tile's own. When the CTA's part of the sequence ends, the warpgroup
 // of its last tile adds the other's O, handed over through TMEM.
 //
-// Bound by HBM: 64 sequences of 512 to 8192 tokens (581 MB of E4M3 codes and scales, 8 KV
-// heads of 128, 4 query heads each) in 98 to 102 us with the merge, 5.7 to 5.9 TB/s; the
-// plain copy rate would take 90. One sequence of 32768 tokens (67 MB): 18.6 us, of which
-// some 8 are start-up and merge. With 8 query heads a group the softmax takes as long as
-// the copies: 32 sequences of 16384 tokens at 5.0 TB/s.
+// Bound by HBM up to 8 query rows: 64 sequences of 512 to 8192 tokens (581 MB of E4M3
+// codes and scales, 8 KV heads of 128, 4 query heads each) in 99 us with the merge,
+// replayed, 5.9 TB/s, and 101 to 106 us a call with other inputs each time; the plain copy
+// rate would take 90. One sequence of 32768 tokens (67 MB): 19.2 us, of which some 8 are
+// start-up and merge. 32 sequences of 16384 tokens with 8 query heads a group: 195 us E4M3
+// and 200 int8, 5.5 and 5.4 TB/s. With 16 rows a thread, one CTA an SM, the softmax sets the
+// pace: 8 sequences of 8192 tokens with 16 query heads a group in 58 us (E4M3) and 67 (int8),
+// 2.3 and 2.0 TB/s. int8's third digit of P costs 2 % up to 8 rows and 10 % at 16.
 #pragma once
 
 #include "decode.cuh"
@@ -448,7 +451,8 @@ __global__ void __launch_bounds__(kQ8Threads, DecodeQ8Smem<D, NH, GP, I8>::kBloc
     }
     const int per_group = __shfl_sync(0xffffffffu, incl, 31);
     const int total = per_group * p.groups;
-    // at least two tiles for each team (so no team without one between two parts): a cut costs as much as a tile
+    // where tiles are few, about two a team, since a cut costs as much as a tile; every team that works has one at
+    // least, so none lies without work between two parts of a sequence
     const int teams = min(p.whole ? total : (total + 1) / 2, p.teams);
     const int quot = teams > 0 ? total / teams : 0, extra = total - quot * teams;   // the first `extra` have one more
     const bool work = team < teams;
@@ -1034,9 +1038,9 @@ __global__ void __launch_bounds__(kQ8Threads, DecodeQ8Smem<D, NH, GP, I8>::kBloc
 // it holds one; its other parts are the first ones of the same lane in the following teams. Bound by
 // latency (its loads are a few KB a CTA, out of L2), so a CTA's four warps take sixteen parts each at a
 // time, all sixteen in flight, a lane D / 32 neighbouring dimensions, and a sequence of at most sixteen
-// parts ends in warp 0 without an exchange. One thread a dimension over all parts, eight in flight, made
-// a call of one sequence of 32768 tokens 19.5 us long with 8 KV heads (37 parts; 18.5 so) and 17.1 with
-// one (148 parts; 13.8 so); a warp a row over all parts 21.9 with 8 KV heads. Merged instead by the
+// parts ends in warp 0 without an exchange. When they were tried, one thread a dimension over all parts, eight in
+// flight, made a call of one sequence of 32768 tokens 19.5 us long with 8 KV heads (37 parts; 18.5 so) and 17.1
+// with one (148 parts; 13.8 so); a warp a row over all parts 21.9 with 8 KV heads. Merged instead by the
 // decode CTA that finishes the last part, found with a counter in the workspace, a call saves this
 // launch but took longer (39 us against 21 when it was tried, and 117 against 102 for 64 sequences): a
 // fence and two dependent loads take microseconds while the other CTAs stream.

@@ -100,8 +100,9 @@ __device__ __forceinline__ void q8_values4(uint32_t four, float (&v)[4]) {
 // their codes are read and rounded again to the new scale. Heads are innermost
 // over the warps of the grid, so neighbouring warps read neighbouring 2 D bytes.
 // Bound by HBM, and by its instructions nearly as much: 201 MB (8 prompts of 4096
-// tokens, 8 heads of 128, int8) in 35 us, 5.7 TB/s. Maxima of packed bf16 bits and
-// conversions without clamps took it there from 55 us, two bits of it by 64 registers
+// tokens, 8 heads of 128, int8) in 34.2 us, 5.9 TB/s, replayed on the same tokens, and
+// 38 to 39 us a call with others each time. Maxima of packed bf16 bits and
+// conversions without clamps took it there from 55 us, some of it by 64 registers
 // (32 warps an SM); a unit a warp, or its two copies in one thread, would read no less.
 template <int D, bool I8, int SEGS>
 __global__ void __launch_bounds__(256, SEGS == 1 ? 4 : 2) kv_append_q8_kernel(const KvAppendQ8Params p) {

@@ -393,9 +393,10 @@ __device__ __forceinline__ int pf_count_skipped(const PrefillParams& p, int jt, 
 // values lie in order in one tensor [B][capacity][Hkv][D] (tm_k / tm_v as in the
 // unpaged prefill), so a tile is D / 64 copies instead of D / 8: the 32 copies of a
 // K/V tile pair from 16-token pages take longer to issue than its products (4 sequences
-// of 2048 new tokens after up to 6144, 32 heads on 8 of D = 128, 8-bit cache: 576 us
-// with the widening, 790 us over 16-token pages of widened keys and values). The LSE of a row that
-// sees a NaN is NaN here.
+// of 2048 new tokens after up to 6144, 32 heads on 8 of D = 128, 8-bit cache: 577 us
+// with the widening, 790 us over 16-token pages of widened keys and values, both a few
+// calls at the full 1965 MHz; calls for seconds on end run at the power cap's 1660 MHz and
+// take 664, on the same inputs as on others). The LSE of a row that sees a NaN is NaN here.
 // CUT (with CONTIG): each item's key tiles are cut into parts (pf_part_tiles), a CTA
 // each, which prefill_merge_kernel merges: for few items, whose tiles one after another
 // leave most SMs idle.

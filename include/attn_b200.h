@@ -326,8 +326,8 @@ int attn_decode_paged_fp8(const void* q, const void* k_codes, const void* v_code
  *   scales  [num_pages][page_size / scale_block][Hkv] fp32: slots
  *           [i * scale_block, (i + 1) * scale_block) of a page share scale i of
  *           their head. Finite and >= 0; any such value is read, the library
- *           writes powers of two. A NaN (or negative V) scale makes its block
- *           read as NaN: results that see the block are NaN.
+ *           writes powers of two. A NaN scale makes its block read as NaN:
+ *           results that see the block are NaN. A negative scale is not allowed.
  *   scale_block  16, 32, 64, 128 or 256, at most page_size
  * Four entry points make a serving loop: attn_kv_append_q8 writes new tokens,
  * attn_decode_paged_q8 and attn_prefill_paged_q8 attend over the cache,
@@ -424,7 +424,9 @@ int attn_decode_paged_q8(const void* q, const void* k_codes, const void* v_codes
  * give equal bits). A table trimmed to the pages in use keeps the workspace
  * small. Returns 0 for invalid arguments or an overflowing size. A key or value
  * that reads as NaN or infinity makes o and the LSE of the queries that see it NaN
- * (all dimensions) and no others.
+ * (all dimensions) and no others. As in attn_prefill_paged, a row's products with V
+ * are summed in fp32 with weights of up to 2^8 before they are divided, so values
+ * whose sum over the row's tokens passes 2^119 may overflow to infinity.
  */
 size_t attn_prefill_paged_q8_workspace_bytes(int B, int Hkv, int D, int max_pages_per_seq, int page_size);
 int attn_prefill_paged_q8(const void* q, const void* k_codes, const void* v_codes, const float* k_scales,
